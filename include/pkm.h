@@ -283,6 +283,73 @@ int pkm_slot_usage(const pkm_shape* s, const int32_t* indices, unsigned long lon
                    void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The transformer block around the layer ("Large Memory Layers with Product Keys":
+ * the memory takes the place of a feed-forward sub-layer of a transformer and is
+ * trained end-to-end with it): layer norm before a sub-layer, the dense sub-layers,
+ * and the optimizer step. Conventions as above (caller-owned contiguous device
+ * arrays, 16-byte aligned; asynchronous on `stream`; the device that owns the arrays
+ * is current; arguments validated before any launch). Calls take no lock that
+ * outlives them and share no scratch, so calls on different streams may overlap if
+ * their workspaces and outputs differ.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Layer norm sizes and types; every *_dtype is a pkm_dtype. */
+typedef struct {
+  int64_t rows;       /* rows (tokens); 0 is allowed, and then the per-row pointers may be NULL */
+  int32_t d;          /* row length, 1 <= d <= 16384 (PKM_ERR_UNSUPPORTED above) */
+  int32_t x_dtype;    /* x and sum */
+  int32_t add_dtype;  /* add; in the backward grad_sum */
+  int32_t y_dtype;    /* y; in the backward grad_y */
+  int32_t grad_dtype; /* grad_x (backward only) */
+  float eps;          /* added to the variance */
+} pkm_norm_shape;
+
+/*
+ * Layer norm, with the residual stream's addition before it:
+ *   h = x + add (added in fp32, rounded to x's type; h = x when add is NULL)
+ *   mean = (1/d) sum_j h_j,  rstd = 1 / sqrt((1/d) sum_j (h_j - mean)^2 + eps)
+ *   y_j = (h_j - mean) rstd gamma_j + beta_j
+ *   x      [rows][d]  x_dtype         add   [rows][d]  add_dtype, may be NULL
+ *   gamma, beta  [d]  fp32            (beta may be NULL: no bias)
+ * Outputs (overwritten):
+ *   y      [rows][d]  y_dtype
+ *   sum    [rows][d]  x_dtype         h; required with add, must be NULL without
+ *   mean, rstd  [rows] fp32           each may be NULL
+ * sum or y may be the same array as x or add where the types are equal (in place);
+ * arrays overlap in no other way. Statistics are computed in fp32 from the row held
+ * on chip, the variance from the centred values.
+ */
+int pkm_layernorm_forward(const pkm_norm_shape* s, const void* x, const void* add,
+                          const float* gamma, const float* beta, void* y, void* sum, float* mean,
+                          float* rstd, void* stream);
+
+/* Bytes of workspace pkm_layernorm_backward needs; 0 if the shape is invalid. Only rows
+ * and d are read. */
+size_t pkm_norm_workspace_size(const pkm_norm_shape* s);
+
+/*
+ * Backward of pkm_layernorm_forward. x is the normalised array (sum where there was an
+ * add), mean and rstd are the forward's. With xhat = (x - mean) rstd, t = grad_y gamma:
+ *   grad_x = rstd (t - (1/d) sum_j t_j - xhat (1/d) sum_j t_j xhat_j) + grad_sum
+ *   grad_gamma = sum_rows grad_y xhat,   grad_beta = sum_rows grad_y
+ *   grad_y [rows][d] y_dtype, x [rows][d] x_dtype, mean, rstd [rows] and gamma [d] fp32
+ *   grad_sum [rows][d] add_dtype: gradient that reaches the residual stream past the
+ *            norm; may be NULL
+ *   grad_x [rows][d] grad_dtype: overwritten. It is the gradient of x and of add alike.
+ *            It may be the same array as grad_y or grad_sum where the types are equal.
+ *   grad_gamma, grad_beta [d] fp32: overwritten (zero when rows is 0); each may be NULL
+ * Column sums are in fp32 in a fixed order: the result is bit-for-bit the same on every
+ * run. workspace: pkm_norm_workspace_size(s) bytes, 256-byte aligned.
+ */
+int pkm_layernorm_backward(const pkm_norm_shape* s, const void* grad_y, const void* x,
+                           const float* mean, const float* rstd, const float* gamma,
+                           const void* grad_sum, void* grad_x, float* grad_gamma,
+                           float* grad_beta, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
  * Synchronises `stream`, reads the status word that the kernels of the last call
  * on this workspace wrote (each call clears it when it starts), clears it and
  * returns PKM_OK, PKM_ERR_DEVICE or PKM_ERR_CUDA. This is the only entry point

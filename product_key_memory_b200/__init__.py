@@ -31,7 +31,8 @@ _STATUS = {0: "PKM_OK", -1: "PKM_ERR_INVALID_ARG", -2: "PKM_ERR_UNSUPPORTED",
 EXPORTED = ("pkm_workspace_size", "pkm_forward", "pkm_backward_values", "pkm_device_status",
             "pkm_trace_enable", "pkm_trace_read", "pkm_status_string",
             "pkm_backward_values_noalloc", "pkm_slot_usage", "pkm_backward",
-            "pkm_forward_train", "pkm_backward_train", "pkm_set_option", "pkm_get_option")
+            "pkm_forward_train", "pkm_backward_train", "pkm_set_option", "pkm_get_option",
+            "pkm_norm_workspace_size", "pkm_layernorm_forward", "pkm_layernorm_backward")
 
 
 class PKMError(RuntimeError):
@@ -45,6 +46,12 @@ class pkm_shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int64), ("d_model", ctypes.c_int32), ("H", ctypes.c_int32),
                 ("dq", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32),
                 ("v", ctypes.c_int32), ("dtype", ctypes.c_int32), ("bn_eps", ctypes.c_float)]
+
+
+class pkm_norm_shape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("d", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
+                ("add_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -87,6 +94,13 @@ def lib() -> ctypes.CDLL:
         L.pkm_set_option.restype = ctypes.c_int
         L.pkm_get_option.argtypes = [ctypes.c_int]
         L.pkm_get_option.restype = ctypes.c_int
+        N = ctypes.POINTER(pkm_norm_shape)
+        L.pkm_norm_workspace_size.argtypes = [N]
+        L.pkm_norm_workspace_size.restype = ctypes.c_size_t
+        L.pkm_layernorm_forward.argtypes = [N] + [P] * 9
+        L.pkm_layernorm_forward.restype = ctypes.c_int
+        L.pkm_layernorm_backward.argtypes = [N] + [P] * 10 + [ctypes.c_size_t, P]
+        L.pkm_layernorm_backward.restype = ctypes.c_int
         L.pkm_status_string.argtypes = [ctypes.c_int]
         L.pkm_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -358,3 +372,185 @@ def pkm_trace_read(pass_: int = 0, max_stages: int = 4):
     if rc != PKM_OK:
         raise PKMError("pkm_trace_read", rc)
     return list(ms), int(calls.value), int(launches.value)
+
+
+# ---------------------------------------------------------------------------------------
+# The transformer block around the layer. These calls check the tensors they are given
+# (device, type, shape, contiguity: ValueError) and run on the device of their first
+# tensor, whichever device is current.
+# ---------------------------------------------------------------------------------------
+_DTYPES = {torch.float32: PKM_F32, torch.bfloat16: PKM_BF16}
+
+
+def _dtype(t) -> int:
+    """pkm_dtype of a torch type (or a pkm_dtype itself)."""
+    if isinstance(t, int):
+        return t
+    if t not in _DTYPES:
+        raise ValueError("libpkm takes float32 and bfloat16, not %s" % t)
+    return _DTYPES[t]
+
+
+def _check(name: str, t: torch.Tensor, shape, dtype, device) -> None:
+    """t is a contiguous device tensor of this shape, type (None: fp32 or bf16) and device."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if dtype is None:
+        _dtype(t.dtype)
+    elif t.dtype != dtype:
+        raise ValueError("%s: %s, expected %s" % (name, t.dtype, dtype))
+    if not t.is_cuda:
+        raise ValueError("%s: libpkm takes device tensors" % name)
+    if t.device != device:
+        raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
+    if not t.is_contiguous():
+        raise ValueError("%s: libpkm takes contiguous tensors" % name)
+
+
+class _Call:
+    """The device and stream of one call: makes `device` current while it lasts, and keeps
+    what the call allocates from being reused before `stream` is done with it."""
+
+    def __init__(self, device: torch.device, stream):
+        self.guard = torch.cuda.device(device)
+        self.device = device
+        self.given = stream
+
+    def __enter__(self):
+        self.guard.__enter__()
+        current = torch.cuda.current_stream(self.device)
+        self.stream = current if self.given is None else self.given
+        self.other = self.stream != current
+        return self
+
+    def __exit__(self, *exc):
+        return self.guard.__exit__(*exc)
+
+    def empty(self, shape, dtype) -> torch.Tensor:
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if self.other:
+            t.record_stream(self.stream)
+        return t
+
+    @property
+    def handle(self):
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def make_norm_shape(rows, d, x_dtype=PKM_F32, add_dtype=PKM_F32, y_dtype=PKM_F32,
+                    grad_dtype=PKM_F32, eps=1e-5) -> pkm_norm_shape:
+    return pkm_norm_shape(int(rows), int(d), _dtype(x_dtype), _dtype(add_dtype), _dtype(y_dtype),
+                          _dtype(grad_dtype), float(eps))
+
+
+def alloc_norm_workspace(shape: pkm_norm_shape, device=None) -> torch.Tensor:
+    """Scratch of pkm_layernorm_backward for this many rows of this width."""
+    n = int(lib().pkm_norm_workspace_size(ctypes.byref(shape)))
+    if n == 0:
+        raise PKMError("pkm_norm_workspace_size", -1)
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def pkm_layernorm_forward(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Tensor],
+                          add: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                          out_dtype: Optional[torch.dtype] = None, want_stats: bool = True,
+                          out: Optional[torch.Tensor] = None,
+                          sum_out: Optional[torch.Tensor] = None, stream=None):
+    """Layer norm of the rows of x + add: (y, h, mean, rstd).
+
+    x [rows][d] and add [rows][d] are fp32 or bf16 each, gamma and beta [d] fp32 (beta may
+    be None). h is x + add in x's type (x itself without add): the new residual stream. y has
+    type out_dtype (x's by default). mean and rstd [rows] fp32 are what
+    pkm_layernorm_backward takes; None unless want_stats. out and sum_out receive y and h
+    and may be x or add themselves (in place) where the types are equal."""
+    if x.dim() != 2:
+        raise ValueError("x must be [rows][d]")
+    rows, d = x.shape
+    dev = x.device
+    _check("x", x, (rows, d), None, dev)
+    _check("gamma", gamma, (d,), torch.float32, dev)
+    if beta is not None:
+        _check("beta", beta, (d,), torch.float32, dev)
+    if add is not None:
+        _check("add", add, (rows, d), None, dev)
+    elif sum_out is not None:
+        raise ValueError("sum_out without add")
+    if out is not None:
+        _check("out", out, (rows, d), out_dtype, dev)
+        out_dtype = out.dtype
+    if sum_out is not None:
+        _check("sum_out", sum_out, (rows, d), x.dtype, dev)
+    out_dtype = out_dtype or x.dtype
+    shape = make_norm_shape(rows, d, x.dtype, PKM_F32 if add is None else add.dtype, out_dtype,
+                            PKM_F32, eps)
+    with _Call(dev, stream) as c:
+        if out is None:
+            out = c.empty((rows, d), out_dtype)
+        if sum_out is None and add is not None:
+            sum_out = c.empty((rows, d), x.dtype)
+        mean = c.empty(rows, torch.float32) if want_stats else None
+        rstd = c.empty(rows, torch.float32) if want_stats else None
+        rc = lib().pkm_layernorm_forward(ctypes.byref(shape), _addr(x), _addr(add), _addr(gamma),
+                                         _addr(beta), _addr(out), _addr(sum_out), _addr(mean),
+                                         _addr(rstd), c.handle)
+    if rc != PKM_OK:
+        raise PKMError("pkm_layernorm_forward", rc)
+    return out, x if add is None else sum_out, mean, rstd
+
+
+def pkm_layernorm_backward(grad_y: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
+                           rstd: torch.Tensor, gamma: torch.Tensor,
+                           grad_sum: Optional[torch.Tensor] = None,
+                           grad_dtype: Optional[torch.dtype] = None,
+                           grad_x: Optional[torch.Tensor] = None,
+                           grad_gamma: Optional[torch.Tensor] = None,
+                           grad_beta: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, stream=None):
+    """Backward of pkm_layernorm_forward: (grad_x, grad_gamma, grad_beta).
+
+    grad_y [rows][d] fp32 or bf16; x, mean, rstd: the forward's h, mean and rstd; grad_sum
+    [rows][d] fp32 or bf16: the gradient that reaches h past the norm (added to grad_x).
+    grad_x has type grad_dtype (grad_y's by default) and may be grad_y or grad_sum itself;
+    grad_gamma and grad_beta [d] are fp32 and overwritten."""
+    if x.dim() != 2:
+        raise ValueError("x must be [rows][d]")
+    rows, d = x.shape
+    dev = x.device
+    _check("x", x, (rows, d), None, dev)
+    _check("grad_y", grad_y, (rows, d), None, dev)
+    _check("mean", mean, (rows,), torch.float32, dev)
+    _check("rstd", rstd, (rows,), torch.float32, dev)
+    _check("gamma", gamma, (d,), torch.float32, dev)
+    if grad_sum is not None:
+        _check("grad_sum", grad_sum, (rows, d), None, dev)
+    if grad_x is not None:
+        _check("grad_x", grad_x, (rows, d), grad_dtype, dev)
+        grad_dtype = grad_x.dtype
+    grad_dtype = grad_dtype or grad_y.dtype
+    for name, t in (("grad_gamma", grad_gamma), ("grad_beta", grad_beta)):
+        if t is not None:
+            _check(name, t, (d,), torch.float32, dev)
+    shape = make_norm_shape(rows, d, x.dtype, PKM_F32 if grad_sum is None else grad_sum.dtype,
+                            grad_y.dtype, grad_dtype)
+    with _Call(dev, stream) as c:
+        if grad_x is None:
+            grad_x = c.empty((rows, d), grad_dtype)
+        if grad_gamma is None:
+            grad_gamma = c.empty(d, torch.float32)
+        if grad_beta is None:
+            grad_beta = c.empty(d, torch.float32)
+        if workspace is None:
+            n = int(lib().pkm_norm_workspace_size(ctypes.byref(shape)))
+            workspace = c.empty(max(n, 1), torch.uint8)
+        rc = lib().pkm_layernorm_backward(ctypes.byref(shape), _addr(grad_y), _addr(x),
+                                          _addr(mean), _addr(rstd), _addr(gamma), _addr(grad_sum),
+                                          _addr(grad_x), _addr(grad_gamma), _addr(grad_beta),
+                                          _ptr(workspace),
+                                          workspace.numel() * workspace.element_size(), c.handle)
+    if rc != PKM_OK:
+        raise PKMError("pkm_layernorm_backward", rc)
+    return grad_x, grad_gamma, grad_beta

@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "../../include/pkm.h"
+#include "pkm_block.h"
 #include "pkm_common.cuh"
 #include "pkm_kernels.h"
 #include "pkm_tc.h"
@@ -366,6 +367,13 @@ int side_stream(pkm::SideStream* side) {
 }
 
 }  // namespace
+
+namespace pkm {
+void count_launches(int n) {
+  std::lock_guard<std::mutex> lk(g_trace_mu);
+  g_launches += n;
+}
+}  // namespace pkm
 
 extern "C" {
 

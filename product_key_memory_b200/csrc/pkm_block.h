@@ -1,0 +1,35 @@
+// pkm_block.h -- internal launcher interface of the transformer-block operators (layer
+// norm, dense layer, AdamW) between pkm_block_api.cu and the kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace pkm {
+
+// Adds n to the library's launch counter (pkm_trace_read).
+void count_launches(int n);
+
+// ---------------------------------------------------------------- layer norm
+constexpr int kNormMaxD = 16384;
+
+struct NormArgs {
+  int64_t rows;
+  int d;
+  int x_dtype, add_dtype, y_dtype, grad_dtype;
+  float eps;
+};
+
+cudaError_t launch_layernorm_forward(const NormArgs& a, const void* x, const void* add,
+                                     const float* gamma, const float* beta, void* y, void* sum,
+                                     float* mean, float* rstd, cudaStream_t st);
+
+// Partial column sums of the backward: blocks (at most) x [2][d] fp32.
+int norm_backward_blocks(int64_t rows, int d);
+cudaError_t launch_layernorm_backward(const NormArgs& a, const void* grad_y, const void* x,
+                                      const float* mean, const float* rstd, const float* gamma,
+                                      const void* grad_sum, void* grad_x, float* grad_gamma,
+                                      float* grad_beta, float* part, cudaStream_t st);
+
+}  // namespace pkm

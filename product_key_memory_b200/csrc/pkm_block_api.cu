@@ -1,0 +1,106 @@
+// pkm_block_api.cu -- the extern "C" entry points of the transformer-block operators
+// declared in include/pkm.h: argument validation and launches. Each call is an NVTX range
+// of its name; the stage trace covers the layer's own passes only.
+#include <math.h>
+
+#include <nvtx3/nvToolsExt.h>
+
+#include "../../include/pkm.h"
+#include "pkm_block.h"
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+bool is_dtype(int t) { return t == PKM_F32 || t == PKM_BF16; }
+
+template <int N>
+bool all_aligned16(const void* const (&ptrs)[N]) {
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return false;
+  return true;
+}
+
+struct Range {
+  explicit Range(const char* name) { nvtxRangePushA(name); }
+  ~Range() { nvtxRangePop(); }
+};
+
+int finish(cudaError_t e, int launches) {
+  if (e != cudaSuccess) return PKM_ERR_CUDA;
+  pkm::count_launches(launches);
+  return PKM_OK;
+}
+
+// rows and d, which every call of the norm reads.
+int validate_norm_size(const pkm_norm_shape* s) {
+  if (!s || s->rows < 0 || s->d < 1) return PKM_ERR_INVALID_ARG;
+  if (s->d > pkm::kNormMaxD || s->rows > 0x7fffffffLL) return PKM_ERR_UNSUPPORTED;
+  return PKM_OK;
+}
+
+int validate_norm(const pkm_norm_shape* s, bool has_add) {
+  const int rc = validate_norm_size(s);
+  if (rc != PKM_OK) return rc;
+  if (!is_dtype(s->x_dtype) || !is_dtype(s->y_dtype) || (has_add && !is_dtype(s->add_dtype)))
+    return PKM_ERR_INVALID_ARG;
+  return PKM_OK;
+}
+
+pkm::NormArgs norm_args(const pkm_norm_shape* s) {
+  return {s->rows, s->d, s->x_dtype, s->add_dtype, s->y_dtype, s->grad_dtype, s->eps};
+}
+
+}  // namespace
+
+extern "C" {
+
+int pkm_layernorm_forward(const pkm_norm_shape* s, const void* x, const void* add,
+                          const float* gamma, const float* beta, void* y, void* sum, float* mean,
+                          float* rstd, void* stream) {
+  const int rc = validate_norm(s, add != nullptr);
+  if (rc != PKM_OK) return rc;
+  if (!(s->eps >= 0.f) || s->eps > 1e30f) return PKM_ERR_INVALID_ARG;
+  if (!gamma || (s->rows > 0 && (!x || !y || (add != nullptr) != (sum != nullptr))))
+    return PKM_ERR_INVALID_ARG;
+  if (!all_aligned16({x, add, gamma, beta, y, sum, mean, rstd})) return PKM_ERR_UNSUPPORTED;
+  if (s->rows == 0) return PKM_OK;
+  const Range range("pkm.layernorm_forward");
+  return finish(pkm::launch_layernorm_forward(norm_args(s), x, add, gamma, beta, y, sum, mean,
+                                              rstd, static_cast<cudaStream_t>(stream)),
+                1);
+}
+
+size_t pkm_norm_workspace_size(const pkm_norm_shape* s) {
+  if (validate_norm_size(s) != PKM_OK) return 0;
+  return static_cast<size_t>(pkm::norm_backward_blocks(s->rows, s->d)) * 2 * s->d * sizeof(float);
+}
+
+int pkm_layernorm_backward(const pkm_norm_shape* s, const void* grad_y, const void* x,
+                           const float* mean, const float* rstd, const float* gamma,
+                           const void* grad_sum, void* grad_x, float* grad_gamma,
+                           float* grad_beta, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  const int rc = validate_norm(s, grad_sum != nullptr);
+  if (rc != PKM_OK) return rc;
+  if (!is_dtype(s->grad_dtype)) return PKM_ERR_INVALID_ARG;
+  if (!gamma || (s->rows > 0 && (!grad_y || !x || !mean || !rstd || !grad_x)))
+    return PKM_ERR_INVALID_ARG;
+  if (!all_aligned16({grad_y, x, mean, rstd, gamma, grad_sum, grad_x, grad_gamma, grad_beta}))
+    return PKM_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < pkm_norm_workspace_size(s) || !aligned256(workspace))
+    return PKM_ERR_WORKSPACE;
+  const Range range("pkm.layernorm_backward");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (s->rows == 0) {
+    for (float* g : {grad_gamma, grad_beta})
+      if (g && cudaMemsetAsync(g, 0, sizeof(float) * s->d, st) != cudaSuccess) return PKM_ERR_CUDA;
+    return PKM_OK;
+  }
+  return finish(pkm::launch_layernorm_backward(norm_args(s), grad_y, x, mean, rstd, gamma,
+                                               grad_sum, grad_x, grad_gamma, grad_beta,
+                                               static_cast<float*>(workspace), st),
+                grad_gamma || grad_beta ? 2 : 1);
+}
+
+}  // extern "C"

@@ -1,0 +1,111 @@
+// pkm_elem.cuh -- typed vector loads and stores of the transformer-block kernels: V
+// consecutive elements (8: 16-byte accesses, 1: any alignment) of fp32 or bf16 arrays,
+// widened to fp32. Loads are ordinary (not the read-only path): several operators may
+// run in place.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "pkm_common.cuh"
+
+namespace pkm {
+
+struct F32 {
+  using T = float;
+};
+struct BF16 {
+  using T = __nv_bfloat16;
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// V elements of type E in their stored form (a load in flight costs only its bytes).
+template <typename E, int V> struct Raw;
+template <> struct Raw<F32, 8> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    a = __ldcs(q);
+    b = __ldcs(q + 1);
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+};
+template <> struct Raw<BF16, 8> {
+  uint4 a;
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    a = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i));
+  }
+  __device__ __forceinline__ void get(float* f) const { Vec<uint16_t>::widen(a, f); }
+};
+template <> struct Raw<F32, 1> {
+  float a;
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    a = __ldcs(static_cast<const float*>(p) + i);
+  }
+  __device__ __forceinline__ void get(float* f) const { f[0] = a; }
+};
+template <> struct Raw<BF16, 1> {
+  uint16_t a;
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    a = __ldcs(static_cast<const unsigned short*>(p) + i);
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    f[0] = __uint_as_float(static_cast<uint32_t>(a) << 16);
+  }
+};
+
+template <typename E, int V> struct Out;
+template <> struct Out<F32, 8> {
+  __device__ __forceinline__ static void store(void* p, int64_t i, const float* f) {
+    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+    q[0] = make_float4(f[0], f[1], f[2], f[3]);
+    q[1] = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
+template <> struct Out<BF16, 8> {
+  __device__ __forceinline__ static void store(void* p, int64_t i, const float* f) {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
+        make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                   pack_bf16(f[6], f[7]));
+  }
+};
+template <> struct Out<F32, 1> {
+  __device__ __forceinline__ static void store(void* p, int64_t i, const float* f) {
+    static_cast<float*>(p)[i] = f[0];
+  }
+};
+template <> struct Out<BF16, 1> {
+  __device__ __forceinline__ static void store(void* p, int64_t i, const float* f) {
+    static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(f[0]);
+  }
+};
+
+// fp32 parameter vectors, read by every row (cached).
+template <int V>
+__device__ __forceinline__ void load_param(const float* p, int i, float* f) {
+  if (V == 8) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p + i));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p + i) + 1);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  } else {
+    f[0] = __ldg(p + i);
+  }
+}
+
+// The value as an array of type E holds it.
+template <typename E> __device__ __forceinline__ float rounded(float x);
+template <> __device__ __forceinline__ float rounded<F32>(float x) { return x; }
+template <> __device__ __forceinline__ float rounded<BF16>(float x) {
+  return __bfloat162float(__float2bfloat16_rn(x));
+}
+
+}  // namespace pkm
