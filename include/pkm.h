@@ -349,6 +349,66 @@ int pkm_layernorm_backward(const pkm_norm_shape* s, const void* grad_y, const vo
                            float* grad_beta, void* workspace, size_t workspace_bytes,
                            void* stream);
 
+/* One tensor of an AdamW step. */
+typedef struct {
+  void* param;          /* [n] param_dtype, updated */
+  void* grad;           /* [n] grad_dtype; set to zero after it was read with zero_grad */
+  float* master;        /* [n] fp32 copy that carries the parameter: updated, and param becomes
+                           its rounding. NULL: param carries itself */
+  void* m;              /* first moment: [n] fp32, or e4m3 codes with state_bits 8 */
+  void* v;              /* second moment: [n] fp32, or e4m3 codes of its square root with
+                           state_bits 8 */
+  float* m_scale;       /* state_bits 8: [ceil(n / 256)] the scale of each 256 elements' codes */
+  float* v_scale;       /* (NULL with state_bits 32) */
+  int64_t n;            /* elements, 0 <= n < 2^38 */
+  int32_t param_dtype;  /* pkm_dtype */
+  int32_t grad_dtype;   /* pkm_dtype */
+  int32_t state_bits;   /* 32 or 8 */
+  float weight_decay;   /* >= 0 */
+  float lr_scale;       /* the tensor's learning rate over the call's, >= 0 */
+} pkm_adamw_tensor;
+
+typedef struct {
+  double lr;            /* >= 0 */
+  double beta1, beta2;  /* in [0, 1) */
+  double eps;           /* > 0 */
+  double grad_scale;    /* gradients are multiplied by it (clipping, loss scaling) */
+  int64_t step;         /* t, 1 for the first step */
+  uint32_t seed;        /* of the dither of 8-bit states */
+  int32_t zero_grad;    /* 1: gradients are cleared for the next step (pkm_backward
+                           accumulates into grad_values) */
+} pkm_adamw_hyper;
+
+/*
+ * One AdamW step (Loshchilov and Hutter, decoupled weight decay) over a list of tensors:
+ *   g = grad grad_scale,  m <- beta1 m + (1 - beta1) g,  v <- beta2 v + (1 - beta2) g^2
+ *   p <- p (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+ * in fp32, with lr = hyper.lr lr_scale. The moments that move p are the new ones before
+ * they are rounded to 8 bits.
+ * 8-bit states (after the block-wise states of Dettmers et al., "8-bit Optimizers via
+ * Block-wise Quantization"): m and r = sqrt(v) as fp8 e4m3 codes, each block of 256
+ * elements (counted from the tensor's start) with its scale s = the smallest power of two,
+ * at least 2^-100, with |value| <= 448 s all over the block (NaN where a value is not
+ * finite: such a block's states are NaN from then on). A value is code * s. A power of two
+ * keeps the codes' grid where it is from one step to the next, so writing an unchanged
+ * value again is exact. m / s is rounded to nearest even. One step moves r by a small part
+ * of a code, which rounding to nearest would drop every time: q = r / s is rounded to a
+ * multiple of ulp, the code spacing at q, after a dither: fl(q + u ulp) to the nearest
+ * multiple, with u = (b - 32767.5) / 65536, b the 16 low (even elements) or high (odd
+ * elements) bits of mix(i / 2 xor key), key = mix(mix(seed + 0x9e3779b9 t) xor
+ * 0x9e3779b9 index), index the tensor's place in the list, mix MurmurHash3's 32-bit
+ * finaliser, all modulo 2^32. What is above 0 stays at least the smallest code, 2^-9. All
+ * zeros (codes and scales) are the initial states.
+ *   dyn: NULL, or three device fp32 {lr, t, grad_scale} read when the step runs, in the
+ *        place of hyper's (t a whole number >= 1): a captured step takes new values at
+ *        every replay.
+ * An array may not appear twice in the list. Tensors with n = 0 are skipped (their index
+ * counts). Arrays behind the list may be freed when the call returns (the list is copied
+ * into the launches).
+ */
+int pkm_adamw_step(const pkm_adamw_tensor* tensors, int64_t count, const pkm_adamw_hyper* hyper,
+                   const float* dyn, void* stream);
+
 /*
  * Synchronises `stream`, reads the status word that the kernels of the last call
  * on this workspace wrote (each call clears it when it starts), clears it and

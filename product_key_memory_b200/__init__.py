@@ -32,7 +32,8 @@ EXPORTED = ("pkm_workspace_size", "pkm_forward", "pkm_backward_values", "pkm_dev
             "pkm_trace_enable", "pkm_trace_read", "pkm_status_string",
             "pkm_backward_values_noalloc", "pkm_slot_usage", "pkm_backward",
             "pkm_forward_train", "pkm_backward_train", "pkm_set_option", "pkm_get_option",
-            "pkm_norm_workspace_size", "pkm_layernorm_forward", "pkm_layernorm_backward")
+            "pkm_norm_workspace_size", "pkm_layernorm_forward", "pkm_layernorm_backward",
+            "pkm_adamw_step")
 
 
 class PKMError(RuntimeError):
@@ -52,6 +53,22 @@ class pkm_norm_shape(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("d", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
                 ("add_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32),
                 ("grad_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class pkm_adamw_tensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("master", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("param_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("state_bits", ctypes.c_int32),
+                ("weight_decay", ctypes.c_float), ("lr_scale", ctypes.c_float)]
+
+
+class pkm_adamw_hyper(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("grad_scale", ctypes.c_double),
+                ("step", ctypes.c_int64), ("seed", ctypes.c_uint32),
+                ("zero_grad", ctypes.c_int32)]
 
 
 _lib = None
@@ -101,6 +118,9 @@ def lib() -> ctypes.CDLL:
         L.pkm_layernorm_forward.restype = ctypes.c_int
         L.pkm_layernorm_backward.argtypes = [N] + [P] * 10 + [ctypes.c_size_t, P]
         L.pkm_layernorm_backward.restype = ctypes.c_int
+        L.pkm_adamw_step.argtypes = [ctypes.POINTER(pkm_adamw_tensor), ctypes.c_int64,
+                                     ctypes.POINTER(pkm_adamw_hyper), P, P]
+        L.pkm_adamw_step.restype = ctypes.c_int
         L.pkm_status_string.argtypes = [ctypes.c_int]
         L.pkm_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -554,3 +574,99 @@ def pkm_layernorm_backward(grad_y: torch.Tensor, x: torch.Tensor, mean: torch.Te
     if rc != PKM_OK:
         raise PKMError("pkm_layernorm_backward", rc)
     return grad_x, grad_gamma, grad_beta
+
+
+ADAMW_BLOCK = 256      # elements that share a scale of 8-bit states
+
+
+def alloc_adamw_state(param: torch.Tensor, bits: int = 32) -> dict:
+    """The initial states of one parameter as the entries make_adamw_tensors takes: m and v in
+    fp32, or (bits=8) as torch.float8_e4m3fn codes with m_scale and v_scale."""
+    if bits not in (32, 8):
+        raise ValueError("bits is 32 or 8")
+    kind = torch.float32 if bits == 32 else torch.float8_e4m3fn
+    state = {k: torch.zeros(param.shape, dtype=kind, device=param.device) for k in ("m", "v")}
+    if bits == 8:
+        blocks = -(-param.numel() // ADAMW_BLOCK)
+        for k in ("m_scale", "v_scale"):
+            state[k] = torch.zeros(blocks, dtype=torch.float32, device=param.device)
+    return state
+
+
+class AdamWTensors:
+    """The list pkm_adamw_step works through (make_adamw_tensors): holds its tensors."""
+
+    def __init__(self, array, tensors, device):
+        self.array, self.tensors, self.device = array, tensors, device
+
+    def __len__(self):
+        return len(self.array)
+
+
+def make_adamw_tensors(tensors) -> AdamWTensors:
+    """The list of an AdamW step, made once for tensors that stay where they are.
+
+    Each entry is a dict: param (fp32 or bf16, updated in place), grad (fp32 or bf16 of its
+    shape), m and v (fp32, or torch.float8_e4m3fn with m_scale and v_scale [ceil(n / 256)]
+    fp32; v then holds the second moment's square root), optionally master (fp32, the copy
+    of a bf16 param that carries it), weight_decay (0) and lr_scale (1). All tensors are
+    contiguous, on one device and distinct."""
+    array = (pkm_adamw_tensor * len(tensors))()
+    device = tensors[0]["param"].device if len(tensors) else torch.device("cuda")
+    kept, spans = [], []
+    for i, t in enumerate(tensors):
+        p = t["param"]
+        n, where = p.numel(), "tensor %d: " % i
+        _check(where + "param", p, p.shape, None, device)
+        _check(where + "grad", t["grad"], p.shape, None, device)
+        bits = 8 if t["m"].dtype == torch.float8_e4m3fn else 32
+        kind = torch.float8_e4m3fn if bits == 8 else torch.float32
+        for k in ("m", "v"):
+            _check(where + k, t[k], p.shape, kind, device)
+        for k in ("m_scale", "v_scale"):
+            if (t.get(k) is not None) != (bits == 8):
+                raise ValueError(where + "%s goes with 8-bit states" % k)
+            if bits == 8:
+                _check(where + k, t[k], (-(-n // ADAMW_BLOCK),), torch.float32, device)
+        if t.get("master") is not None:
+            if p.dtype != torch.bfloat16:
+                raise ValueError(where + "master goes with a bf16 param")
+            _check(where + "master", t["master"], p.shape, torch.float32, device)
+        a = array[i]
+        for k in ("param", "grad", "master", "m", "v", "m_scale", "v_scale"):
+            x = t.get(k)
+            if x is not None:
+                setattr(a, k, x.data_ptr())
+                kept.append(x)
+                if x.numel():
+                    spans.append((x.data_ptr(), x.data_ptr() + x.numel() * x.element_size(),
+                                  where + k))
+        a.n, a.param_dtype, a.grad_dtype = n, _dtype(p.dtype), _dtype(t["grad"].dtype)
+        a.state_bits = bits
+        a.weight_decay = float(t.get("weight_decay", 0.0))
+        a.lr_scale = float(t.get("lr_scale", 1.0))
+    spans.sort()
+    for (_, end, first), (begin, _, second) in zip(spans, spans[1:]):
+        if begin < end:
+            raise ValueError("%s and %s overlap" % (first, second))
+    return AdamWTensors(array, kept, device)
+
+
+def pkm_adamw_step(tensors: AdamWTensors, lr: float, step: int, betas=(0.9, 0.999),
+                   eps: float = 1e-8, grad_scale: float = 1.0, zero_grad: bool = False,
+                   seed: int = 0, dyn: Optional[torch.Tensor] = None, stream=None) -> None:
+    """One AdamW step over a list from make_adamw_tensors: parameters, masters and states are
+    updated in place, gradients cleared with zero_grad. step counts from 1. dyn: three
+    device fp32 [lr, step, grad_scale] that the step reads in the place of the arguments
+    when it runs (for captured steps)."""
+    if not isinstance(tensors, AdamWTensors):
+        raise ValueError("pkm_adamw_step takes a list from make_adamw_tensors")
+    if dyn is not None:
+        _check("dyn", dyn, (3,), torch.float32, tensors.device)
+    h = pkm_adamw_hyper(float(lr), float(betas[0]), float(betas[1]), float(eps),
+                        float(grad_scale), int(step), int(seed) & 0xffffffff, int(bool(zero_grad)))
+    with _Call(tensors.device, stream) as c:
+        rc = lib().pkm_adamw_step(tensors.array, len(tensors), ctypes.byref(h), _addr(dyn),
+                                  c.handle)
+    if rc != PKM_OK:
+        raise PKMError("pkm_adamw_step", rc)

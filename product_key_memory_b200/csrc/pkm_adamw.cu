@@ -1,0 +1,406 @@
+// pkm_adamw.cu -- one AdamW step over a list of tensors, states in fp32 or in 8 bits.
+//
+//   m <- b1 m + (1 - b1) g,  v <- b2 v + (1 - b2) g^2,
+//   p <- p (1 - lr wd) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//
+// Every element is read once and written once, so the step is bound by HBM. The list
+// travels in the kernel's parameters (no device copy of it, nothing to keep alive, and a
+// captured launch holds its own). The tensors' elements are cut into units of kUnit; a
+// block takes units b, b + grid, ... and finds a unit's tensor by its first unit. A
+// warp owns 256 consecutive elements, 8 per lane, which is also the block that shares
+// a scale of 8-bit states: its largest magnitude is one warp reduction of the fp32 bits
+// (ordered like the magnitudes, NaN above all). m, v, r and their 8-bit forms are
+// computed in single operations rounded to nearest (no fused multiply-add), so they are
+// the same bits as the formula evaluated step by step in fp32.
+#include <cuda_fp8.h>
+
+#include <math.h>
+
+#include "pkm_block.h"
+#include "pkm_elem.cuh"
+#include "pkm_tc.h"
+
+namespace pkm {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnit = kThreads * 8;
+
+enum : uint32_t { kParamBf16 = 1, kGradBf16 = 2, kEight = 4, kMaster = 8 };
+
+struct Tensor {
+  void* param;
+  void* grad;
+  float* master;
+  void* m;
+  void* v;
+  float* ms;
+  float* vs;
+  int64_t n;
+  uint32_t first;      // first unit of the launch that belongs to it
+  uint32_t flags;
+  uint32_t key;        // index in the list times the odd constant of the dither's key
+  float keep, step;    // 1 - lr wd and lr / (1 - b1^t); with dyn: wd and lr_scale
+};
+
+template <int CAP>
+struct List {
+  Tensor t[CAP];
+  int count;
+  uint32_t units;
+  float b1, c1, b2, c2, eps, root, grad_scale;   // c = 1 - b, root = 1 / sqrt(1 - b2^t)
+  double db1, db2;
+  uint32_t seed, step32;
+  int zero;
+  const float* dyn;
+};
+
+__host__ __device__ __forceinline__ uint32_t mix32(uint32_t h) {
+  h ^= h >> 16;
+  h *= 0x85ebca6bu;
+  h ^= h >> 13;
+  h *= 0xc2b2ae35u;
+  return h ^ (h >> 16);
+}
+
+constexpr uint32_t kGolden = 0x9e3779b9u;
+
+// Bits of the smallest power of two s >= 2^-100 with |x| <= 448 s, 448 = 1.75 2^8, for the
+// largest |x| of the block by its bits: a mantissa above 1.75 carries into the exponent.
+__device__ __forceinline__ uint32_t scale_bits(uint32_t most) {
+  if (most >= 0x7f800000u) return 0x7fc00000u;
+  const uint32_t b = (most + 0x1fffffu) & 0x7f800000u;
+  const uint32_t low = 27u << 23;   // 2^-100
+  return b < low + (8u << 23) ? low : b - (8u << 23);
+}
+
+__device__ __forceinline__ float inverse_pow2(uint32_t sbits) {
+  return sbits == 0x7fc00000u ? __uint_as_float(sbits) : __uint_as_float((254u << 23) - sbits);
+}
+
+__device__ __forceinline__ void widen8(uint2 codes, float scale, float* f) {
+  const uint32_t w[2] = {codes.x, codes.y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+        static_cast<__nv_fp8x2_storage_t>(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+    const float2 x = __half22float2(__half2(h));
+    f[2 * i] = __fmul_rn(x.x, scale);
+    f[2 * i + 1] = __fmul_rn(x.y, scale);
+  }
+}
+
+__device__ __forceinline__ uint2 narrow8(const float* f) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i], f[4 * i + 1]),
+                                                 __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i + 2], f[4 * i + 3]),
+                                                 __NV_SATFINITE, __NV_E4M3);
+    w[i] = lo | (hi << 16);
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// q = r / s rounded to a multiple of ulp, e4m3's spacing at q, after the dither u ulp, u in
+// (-1/2, 1/2) from 16 bits of the pair's hash. Rounding on q's own grid leaves a q that is
+// a code as it is, powers of two included (the codes below one lie twice as close: rounding
+// q + u ulp to the nearest code would pull such a q down a quarter of the time).
+__device__ __forceinline__ float dithered(float q, uint32_t bits16) {
+  // 2^23 + b exactly, then b / 65536 - 32767.5 / 65536 exactly.
+  const float b = __uint_as_float(0x4b000000u | bits16) - 8388608.f;
+  const float u = fmaf(b, 1.f / 65536.f, -32767.5f / 65536.f);
+  const uint32_t e = max(__float_as_uint(q) & 0x7f800000u, 121u << 23);   // e4m3: at least 2^-6
+  // Adding 1.5 2^23 ulp rounds to a multiple of ulp (ties to even).
+  const float grid = __uint_as_float(e + (20u << 23) + 0x400000u);
+  const float near = __fadd_rn(q, __fmul_rn(u, __uint_as_float(e - (3u << 23))));
+  return q > 0.f ? fmaxf(__fadd_rn(near, grid) - grid, 0x1p-9f) : q;
+}
+
+// Eight elements as loaded.
+struct Eight {
+  uint4 a, b;
+};
+
+__device__ __forceinline__ Eight load8(const void* p, int64_t i, bool bf16) {
+  Eight r;
+  if (bf16) {
+    r.a = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i));
+    r.b = make_uint4(0, 0, 0, 0);
+  } else {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
+    r.a = __ldcs(q);
+    r.b = __ldcs(q + 1);
+  }
+  return r;
+}
+
+__device__ __forceinline__ void widen(const Eight& r, bool bf16, float* f) {
+  if (bf16) {
+    Vec<uint16_t>::widen(r.a, f);
+  } else {
+    Vec<float>::widen(r.a, f);
+    Vec<float>::widen(r.b, f + 4);
+  }
+}
+
+__device__ __forceinline__ void store8(void* p, int64_t i, bool bf16, const float* f) {
+  if (bf16) {
+    __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i),
+           make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                      pack_bf16(f[6], f[7])));
+  } else {
+    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+    __stcs(q, make_float4(f[0], f[1], f[2], f[3]));
+    __stcs(q + 1, make_float4(f[4], f[5], f[6], f[7]));
+  }
+}
+
+__device__ __forceinline__ float load1(const void* p, int64_t i, bool bf16) {
+  return bf16 ? load_elem(static_cast<const uint16_t*>(p), i)
+              : load_elem(static_cast<const float*>(p), i);
+}
+
+__device__ __forceinline__ void store1(void* p, int64_t i, bool bf16, float f) {
+  if (bf16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(f);
+  else static_cast<float*>(p)[i] = f;
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ List<CAP> list) {
+  __shared__ float dynamic[3];   // 1 / (1 - b1^t), 1 / sqrt(1 - b2^t), -
+  float root = list.root, grad_scale = list.grad_scale, lr = 0.f, over = 1.f;
+  uint32_t step32 = list.step32;
+  if (list.dyn) {
+    if (threadIdx.x == 0) {
+      const double t = static_cast<double>(list.dyn[1]);
+      dynamic[0] = static_cast<float>(1.0 / (1.0 - pow(list.db1, t)));
+      dynamic[1] = static_cast<float>(1.0 / sqrt(1.0 - pow(list.db2, t)));
+    }
+    __syncthreads();
+    lr = list.dyn[0];
+    grad_scale = list.dyn[2];
+    step32 = static_cast<uint32_t>(static_cast<int64_t>(list.dyn[1]));
+    over = dynamic[0];
+    root = dynamic[1];
+  }
+  const uint32_t key0 = mix32(list.seed + kGolden * step32);
+  const int lane = threadIdx.x & 31;
+  int cur = 0;
+  uint32_t begin = 0, end = 0;
+  for (uint32_t u = blockIdx.x; u < list.units; u += gridDim.x) {
+    if (u >= end) {   // the last tensor whose first unit is at most u
+      int lo = cur, hi = list.count;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (list.t[mid].first <= u) lo = mid;
+        else hi = mid;
+      }
+      cur = lo;
+      begin = list.t[cur].first;
+      end = cur + 1 < list.count ? list.t[cur + 1].first : list.units;
+    }
+    const Tensor& T = list.t[cur];
+    const int64_t n = T.n;
+    const int64_t i = static_cast<int64_t>(u - begin) * kUnit + threadIdx.x * 8;
+    const int64_t block = i >> 8;
+    if (block * 256 >= n) continue;   // warp-uniform
+    const uint32_t fl = T.flags;
+    const bool pb = (fl & kParamBf16) && !(fl & kMaster), gb = fl & kGradBf16, eight = fl & kEight;
+    void* carrier = (fl & kMaster) ? static_cast<void*>(T.master) : T.param;
+    const bool whole = i + 8 <= n;
+    float p[8], g[8], m[8], v[8];
+    if (whole) {
+      const Eight rg = load8(T.grad, i, gb);
+      const Eight rp = load8(carrier, i, pb);
+      if (eight) {
+        const uint2 rm = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(T.m) + i));
+        const uint2 rv = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(T.v) + i));
+        const float ms = T.ms[block], vs = T.vs[block];
+        widen8(rm, ms, m);
+        widen8(rv, vs, v);
+      } else {
+        const Eight rm = load8(T.m, i, false), rv = load8(T.v, i, false);
+        widen(rm, false, m);
+        widen(rv, false, v);
+      }
+      widen(rg, gb, g);
+      widen(rp, pb, p);
+    } else {
+      const float ms = eight ? T.ms[block] : 0.f, vs = eight ? T.vs[block] : 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool in = i + j < n;
+        g[j] = in ? load1(T.grad, i + j, gb) : 0.f;
+        p[j] = in ? load1(carrier, i + j, pb) : 0.f;
+        if (eight) {
+          const uint32_t cm = in ? static_cast<const uint8_t*>(T.m)[i + j] : 0u;
+          const uint32_t cv = in ? static_cast<const uint8_t*>(T.v)[i + j] : 0u;
+          m[j] = __fmul_rn(__half2float(__half(__nv_cvt_fp8_to_halfraw(cm, __NV_E4M3))), ms);
+          v[j] = __fmul_rn(__half2float(__half(__nv_cvt_fp8_to_halfraw(cv, __NV_E4M3))), vs);
+        } else {
+          m[j] = in ? static_cast<const float*>(T.m)[i + j] : 0.f;
+          v[j] = in ? static_cast<const float*>(T.v)[i + j] : 0.f;
+        }
+      }
+    }
+    float keep = T.keep, step = T.step;
+    if (list.dyn) {
+      const float mine = lr * step;            // lr lr_scale
+      keep = 1.f - mine * keep;
+      step = mine * over;
+    }
+    uint32_t most_m = 0, most_r = 0;
+    float r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float gj = __fmul_rn(g[j], grad_scale);
+      if (eight) v[j] = __fmul_rn(v[j], v[j]);
+      m[j] = __fadd_rn(__fmul_rn(list.b1, m[j]), __fmul_rn(list.c1, gj));
+      v[j] = __fadd_rn(__fmul_rn(list.b2, v[j]), __fmul_rn(__fmul_rn(list.c2, gj), gj));
+      r[j] = __fsqrt_rn(v[j]);
+      p[j] = p[j] * keep - step * (m[j] / fmaf(r[j], root, list.eps));
+      most_m = max(most_m, __float_as_uint(m[j]) & 0x7fffffffu);
+      most_r = max(most_r, __float_as_uint(r[j]) & 0x7fffffffu);
+    }
+    if (eight) {
+      const uint32_t bm = scale_bits(__reduce_max_sync(0xffffffffu, most_m));
+      const uint32_t br = scale_bits(__reduce_max_sync(0xffffffffu, most_r));
+      const float im = inverse_pow2(bm), ir = inverse_pow2(br);
+      const uint32_t key = mix32(key0 ^ T.key);
+      const uint32_t pair = static_cast<uint32_t>(i >> 1);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t h = mix32((pair + j) ^ key);
+        m[2 * j] = __fmul_rn(m[2 * j], im);
+        m[2 * j + 1] = __fmul_rn(m[2 * j + 1], im);
+        v[2 * j] = dithered(__fmul_rn(r[2 * j], ir), h & 0xffffu);
+        v[2 * j + 1] = dithered(__fmul_rn(r[2 * j + 1], ir), h >> 16);
+      }
+      const uint2 cm = narrow8(m), cv = narrow8(v);
+      if (lane == 0) {
+        T.ms[block] = __uint_as_float(bm);
+        T.vs[block] = __uint_as_float(br);
+      }
+      if (whole) {
+        __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(T.m) + i), cm);
+        __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(T.v) + i), cv);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (i + j < n) {
+            static_cast<uint8_t*>(T.m)[i + j] =
+                static_cast<uint8_t>((j < 4 ? cm.x : cm.y) >> (8 * (j & 3)));
+            static_cast<uint8_t*>(T.v)[i + j] =
+                static_cast<uint8_t>((j < 4 ? cv.x : cv.y) >> (8 * (j & 3)));
+          }
+      }
+    }
+    if (whole) {
+      if (!eight) {
+        store8(T.m, i, false, m);
+        store8(T.v, i, false, v);
+      }
+      if (fl & kMaster) store8(T.master, i, false, p);
+      store8(T.param, i, fl & kParamBf16, p);
+      if (list.zero) {
+        const float z[8] = {};
+        store8(T.grad, i, gb, z);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (i + j >= n) continue;
+        if (!eight) {
+          static_cast<float*>(T.m)[i + j] = m[j];
+          static_cast<float*>(T.v)[i + j] = v[j];
+        }
+        if (fl & kMaster) T.master[i + j] = p[j];
+        store1(T.param, i + j, fl & kParamBf16, p[j]);
+        if (list.zero) store1(T.grad, i + j, gb, 0.f);
+      }
+    }
+  }
+}
+
+constexpr int kSmallList = 16;     // 1.5 KB of parameters
+constexpr int kLargeList = 256;    // 25 KB (32,764 bytes is the limit)
+
+template <int CAP>
+cudaError_t launch_list(List<CAP>& list, cudaStream_t st) {
+  const unsigned most = static_cast<unsigned>(sm_count()) * 8;
+  const unsigned grid = list.units < most ? list.units : most;
+  adamw_kernel<CAP><<<grid, kThreads, 0, st>>>(list);
+  return cudaGetLastError();
+}
+
+template <int CAP>
+cudaError_t run_lists(const AdamWTensor* t, int64_t count, const AdamWHyper& h, const float* dyn,
+                      int* launches, cudaStream_t st) {
+  static_assert(sizeof(List<CAP>) <= 32764, "kernel parameters");
+  List<CAP> list;
+  const double fix1 = 1.0 - pow(h.beta1, static_cast<double>(h.step));
+  const double fix2 = 1.0 - pow(h.beta2, static_cast<double>(h.step));
+  list.b1 = static_cast<float>(h.beta1);
+  list.c1 = static_cast<float>(1.0 - h.beta1);
+  list.b2 = static_cast<float>(h.beta2);
+  list.c2 = static_cast<float>(1.0 - h.beta2);
+  list.eps = static_cast<float>(h.eps);
+  list.root = static_cast<float>(1.0 / sqrt(fix2));
+  list.grad_scale = static_cast<float>(h.grad_scale);
+  list.db1 = h.beta1;
+  list.db2 = h.beta2;
+  list.seed = h.seed;
+  list.step32 = static_cast<uint32_t>(h.step);
+  list.zero = h.zero_grad;
+  list.dyn = dyn;
+  list.count = 0;
+  list.units = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (t[i].n > 0) {
+      Tensor& d = list.t[list.count++];
+      d.param = t[i].param;
+      d.grad = t[i].grad;
+      d.master = t[i].master;
+      d.m = t[i].m;
+      d.v = t[i].v;
+      d.ms = t[i].m_scale;
+      d.vs = t[i].v_scale;
+      d.n = t[i].n;
+      d.first = list.units;
+      d.flags = (t[i].param_dtype ? kParamBf16 : 0) | (t[i].grad_dtype ? kGradBf16 : 0) |
+                (t[i].state_bits == 8 ? kEight : 0) | (t[i].master ? kMaster : 0);
+      d.key = static_cast<uint32_t>(i) * kGolden;
+      if (dyn) {
+        d.keep = t[i].weight_decay;
+        d.step = t[i].lr_scale;
+      } else {
+        const double lr = h.lr * t[i].lr_scale;
+        d.keep = static_cast<float>(1.0 - lr * t[i].weight_decay);
+        d.step = static_cast<float>(lr / fix1);
+      }
+      list.units += static_cast<uint32_t>((d.n + kUnit - 1) / kUnit);
+    }
+    // A launch holds CAP tensors and 2^31 units; a tensor has at most 2^27.
+    if (list.count && (list.count == CAP || i + 1 == count || list.units >= 1u << 30)) {
+      const cudaError_t e = launch_list(list, st);
+      if (e != cudaSuccess) return e;
+      ++*launches;
+      list.count = 0;
+      list.units = 0;
+    }
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_adamw(const AdamWTensor* t, int64_t count, const AdamWHyper& h,
+                         const float* dyn, int* launches, cudaStream_t st) {
+  return count <= kSmallList ? run_lists<kSmallList>(t, count, h, dyn, launches, st)
+                             : run_lists<kLargeList>(t, count, h, dyn, launches, st);
+}
+
+}  // namespace pkm

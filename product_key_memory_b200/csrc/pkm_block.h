@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/pkm.h"
+
 namespace pkm {
 
 // Adds n to the library's launch counter (pkm_trace_read).
@@ -31,5 +33,12 @@ cudaError_t launch_layernorm_backward(const NormArgs& a, const void* grad_y, con
                                       const float* mean, const float* rstd, const float* gamma,
                                       const void* grad_sum, void* grad_x, float* grad_gamma,
                                       float* grad_beta, float* part, cudaStream_t st);
+
+// --------------------------------------------------------------------- AdamW
+using AdamWTensor = pkm_adamw_tensor;
+using AdamWHyper = pkm_adamw_hyper;
+// Adds the kernels launched to *launches.
+cudaError_t launch_adamw(const AdamWTensor* t, int64_t count, const AdamWHyper& h,
+                         const float* dyn, int* launches, cudaStream_t st);
 
 }  // namespace pkm

@@ -103,4 +103,38 @@ int pkm_layernorm_backward(const pkm_norm_shape* s, const void* grad_y, const vo
                 grad_gamma || grad_beta ? 2 : 1);
 }
 
+int pkm_adamw_step(const pkm_adamw_tensor* tensors, int64_t count, const pkm_adamw_hyper* h,
+                   const float* dyn, void* stream) {
+  if (!h || count < 0 || (count > 0 && !tensors)) return PKM_ERR_INVALID_ARG;
+  // Written so that a NaN fails. eps must stay above 0 in fp32: an element without
+  // gradients has m = v = 0, and 0 / (0 + eps) has to be 0.
+  const bool rates = h->lr >= 0 && h->lr < 1e30 && h->beta1 >= 0 && h->beta1 < 1 &&
+                     h->beta2 >= 0 && h->beta2 < 1 && h->eps >= 1e-30 && h->eps < 1e30 &&
+                     fabs(h->grad_scale) < 1e30 && h->step >= 1;
+  if (!rates || (h->zero_grad != 0 && h->zero_grad != 1)) return PKM_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(dyn) & 3u) return PKM_ERR_UNSUPPORTED;
+  for (int64_t i = 0; i < count; ++i) {
+    const pkm_adamw_tensor& t = tensors[i];
+    if (t.n < 0 || !is_dtype(t.param_dtype) || !is_dtype(t.grad_dtype) ||
+        (t.state_bits != 32 && t.state_bits != 8))
+      return PKM_ERR_INVALID_ARG;
+    if (!(t.weight_decay >= 0.f && t.weight_decay < 1e30f && t.lr_scale >= 0.f &&
+          t.lr_scale < 1e30f))
+      return PKM_ERR_INVALID_ARG;
+    if (t.n >= 1LL << 38) return PKM_ERR_UNSUPPORTED;
+    if (t.n == 0) continue;
+    const bool eight = t.state_bits == 8;
+    if (!t.param || !t.grad || !t.m || !t.v || (eight && (!t.m_scale || !t.v_scale)) ||
+        (!eight && (t.m_scale || t.v_scale)) || (t.master && t.param_dtype != PKM_BF16))
+      return PKM_ERR_INVALID_ARG;
+    if (!all_aligned16({t.param, t.grad, t.master, t.m, t.v, t.m_scale, t.v_scale}))
+      return PKM_ERR_UNSUPPORTED;
+  }
+  const Range range("pkm.adamw_step");
+  int launches = 0;
+  const cudaError_t e =
+      pkm::launch_adamw(tensors, count, *h, dyn, &launches, static_cast<cudaStream_t>(stream));
+  return finish(e, launches);
+}
+
 }  // extern "C"

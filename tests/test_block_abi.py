@@ -79,3 +79,60 @@ def test_norm_binding_checks_tensors():
         P.make_norm_shape(4, 8, torch.float16)
     with pytest.raises(P.PKMError):
         P.alloc_norm_workspace(P.make_norm_shape(4, 0))
+
+
+def _adamw(t=None, h=None, count=1, dyn=None, tensors=True):
+    a = P.pkm_adamw_tensor(param=OK.value, grad=OK.value, m=OK.value, v=OK.value, n=100,
+                           param_dtype=0, grad_dtype=0, state_bits=32, weight_decay=0.1,
+                           lr_scale=1.0)
+    for k, x in (t or {}).items():
+        setattr(a, k, x)
+    b = P.pkm_adamw_hyper(lr=1e-3, beta1=0.9, beta2=0.98, eps=1e-8, grad_scale=1.0, step=1)
+    for k, x in (h or {}).items():
+        setattr(b, k, x)
+    return P.lib().pkm_adamw_step(ctypes.byref(a) if tensors else None, count, ctypes.byref(b), dyn,
+                                  None)
+
+
+@pytest.mark.parametrize("t,code", [
+    (dict(param=None), -1), (dict(grad=None), -1), (dict(m=None), -1), (dict(v=None), -1),
+    (dict(n=-1), -1), (dict(n=1 << 38), -2), (dict(param_dtype=2), -1), (dict(grad_dtype=-1), -1),
+    (dict(state_bits=16), -1), (dict(state_bits=8), -1),
+    (dict(state_bits=8, m_scale=OK.value), -1), (dict(m_scale=OK.value), -1),
+    (dict(master=OK.value), -1), (dict(weight_decay=-0.1), -1),
+    (dict(weight_decay=math.nan), -1), (dict(lr_scale=-1.0), -1), (dict(lr_scale=math.inf), -1),
+    (dict(param=ODD.value), -2), (dict(grad=ODD.value), -2), (dict(m=ODD.value), -2),
+    (dict(v=ODD.value), -2),
+    (dict(state_bits=8, m_scale=ODD.value, v_scale=OK.value), -2),
+    (dict(param_dtype=1, master=ODD.value), -2)])
+def test_adamw_tensor_refused(t, code):
+    assert _adamw(t) == code
+
+
+@pytest.mark.parametrize("h", [
+    dict(lr=-1.0), dict(lr=math.nan), dict(lr=math.inf), dict(beta1=1.0), dict(beta1=-0.1),
+    dict(beta2=1.0), dict(beta2=math.nan), dict(eps=0.0), dict(eps=math.nan), dict(eps=-1.0),
+    dict(grad_scale=math.inf), dict(grad_scale=math.nan), dict(step=0), dict(step=-3),
+    dict(zero_grad=2)])
+def test_adamw_hyper_refused(h):
+    assert _adamw(h=h) == -1
+
+
+def test_adamw_call_refused():
+    assert _adamw(count=-1) == -1 and _adamw(tensors=False) == -1
+    assert _adamw(dyn=ctypes.c_void_p((1 << 20) + 2)) == -2
+    assert P.lib().pkm_adamw_step(None, 0, None, None, None) == -1
+    assert _adamw(count=0, tensors=False) == 0            # an empty list
+    assert _adamw(dict(n=0, param=None)) == 0             # an empty tensor
+
+
+def test_adamw_binding_checks_tensors():
+    x = torch.zeros(8)
+    with pytest.raises(ValueError):
+        P.make_adamw_tensors([dict(param=x, grad=x, m=x, v=x)])       # host tensors
+    with pytest.raises(ValueError):
+        P.pkm_adamw_step([dict(param=x)], lr=1e-3, step=1)
+    with pytest.raises(ValueError):
+        P.alloc_adamw_state(x, 16)
+    s = P.alloc_adamw_state(torch.zeros(300), 8)
+    assert s["m"].dtype == torch.float8_e4m3fn and s["v_scale"].shape == (2,)
