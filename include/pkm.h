@@ -349,6 +349,59 @@ int pkm_layernorm_backward(const pkm_norm_shape* s, const void* grad_y, const vo
                            float* grad_beta, void* workspace, size_t workspace_bytes,
                            void* stream);
 
+/* Activations of the dense layer: relu; gelu(v) = v Phi(v) with the normal distribution
+ * Phi (not its tanh approximation); silu(v) = v / (1 + exp(-v)). */
+enum { PKM_ACT_NONE = 0, PKM_ACT_RELU = 1, PKM_ACT_GELU = 2, PKM_ACT_SILU = 3 };
+
+/* Dense layer sizes and types. */
+typedef struct {
+  int64_t M;           /* rows (tokens), < 2^31; 0 is allowed, and then the per-row pointers may
+                          be NULL */
+  int32_t N;           /* output width, 1 <= N <= 2^20 */
+  int32_t K;           /* input width, 1 <= K <= 2^20 */
+  int32_t dtype;       /* pkm_dtype of x, W, pre and, in the backward, grad_y */
+  int32_t out_dtype;   /* pkm_dtype of y and residual; in the backward of grad_x */
+  int32_t activation;
+} pkm_linear_shape;
+
+/* Bytes of workspace of pkm_linear_forward (for_backward = 0) or pkm_linear_backward (1);
+ * 0 if the shape is invalid or not supported. */
+size_t pkm_linear_workspace_size(const pkm_linear_shape* s, int for_backward);
+
+/*
+ * Dense layer: pre = x W^T + bias,  y = activation(pre) + residual.
+ *   x [M][K], W [N][K]  dtype;  bias [N] fp32, may be NULL;  residual [M][N] out_dtype, may be
+ *   NULL (or the same array as y: in place)
+ * Outputs (overwritten): y [M][N] out_dtype;  pre [M][N] dtype, may be NULL: what
+ * pkm_linear_backward takes.
+ * Products accumulate in fp32 on the tensor cores. fp32 operands are split into three bf16
+ * planes whose sum is the value to 2^-24, and the products above 2^-24 of the largest are
+ * added; so an infinite operand makes its sums infinite or NaN. y is computed from pre
+ * before pre is rounded. Up to 8 rows take a kernel that streams W once (in fp32
+ * arithmetic). M < 2^31, and M, N and K with M N and M K below 2^38.
+ * workspace: pkm_linear_workspace_size(s, 0) bytes, 256-byte aligned; its status word
+ * (pkm_device_status) records a bounded wait that ran out.
+ */
+int pkm_linear_forward(const pkm_linear_shape* s, const void* x, const void* W, const float* bias,
+                       const void* residual, void* y, void* pre, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * Backward of pkm_linear_forward. With d = grad_y activation'(pre) (relu'(0) = 0):
+ *   grad_x [M][K] out_dtype = d W,  grad_W [N][K] fp32 = d^T x,  grad_bias [N] fp32 = sum_rows d
+ * each overwritten and each may be NULL (not computed). The residual's gradient is grad_y.
+ *   x, W as in the forward; grad_y [M][N] dtype; pre [M][N] dtype as the forward wrote it
+ *   (not read, may be NULL, without an activation)
+ * d is an fp32 value. In fp32 layers it enters the products as three bf16 planes, in bf16
+ * layers with an activation as two (hi + lo, within 2^-17 of d), and as hi alone in a bf16
+ * grad_x, whose own rounding is as large. Column sums add in a fixed order; all results are
+ * bit-for-bit the same on every run.
+ * workspace: pkm_linear_workspace_size(s, 1) bytes, 256-byte aligned, status word as above.
+ */
+int pkm_linear_backward(const pkm_linear_shape* s, const void* x, const void* W,
+                        const void* grad_y, const void* pre, void* grad_x, float* grad_W,
+                        float* grad_bias, void* workspace, size_t workspace_bytes, void* stream);
+
 /* One tensor of an AdamW step. */
 typedef struct {
   void* param;          /* [n] param_dtype, updated */

@@ -25,6 +25,8 @@ PKM_OPT_PATH, PKM_OPT_SUBBATCHES = 0, 1
 PKM_PATH_AUTO, PKM_PATH_TC, PKM_PATH_SIMT, PKM_PATH_SMALL_FUSED, PKM_PATH_SMALL_SPLIT = range(5)
 _PATHS = {"auto": PKM_PATH_AUTO, "tc": PKM_PATH_TC, "simt": PKM_PATH_SIMT,
           "small_fused": PKM_PATH_SMALL_FUSED, "small_split": PKM_PATH_SMALL_SPLIT}
+PKM_ACT_NONE, PKM_ACT_RELU, PKM_ACT_GELU, PKM_ACT_SILU = range(4)
+_ACTS = {"none": PKM_ACT_NONE, "relu": PKM_ACT_RELU, "gelu": PKM_ACT_GELU, "silu": PKM_ACT_SILU}
 _STATUS = {0: "PKM_OK", -1: "PKM_ERR_INVALID_ARG", -2: "PKM_ERR_UNSUPPORTED",
            -3: "PKM_ERR_WORKSPACE", -4: "PKM_ERR_CUDA", -5: "PKM_ERR_DEVICE"}
 
@@ -33,7 +35,8 @@ EXPORTED = ("pkm_workspace_size", "pkm_forward", "pkm_backward_values", "pkm_dev
             "pkm_backward_values_noalloc", "pkm_slot_usage", "pkm_backward",
             "pkm_forward_train", "pkm_backward_train", "pkm_set_option", "pkm_get_option",
             "pkm_norm_workspace_size", "pkm_layernorm_forward", "pkm_layernorm_backward",
-            "pkm_adamw_step")
+            "pkm_adamw_step", "pkm_linear_workspace_size", "pkm_linear_forward",
+            "pkm_linear_backward")
 
 
 class PKMError(RuntimeError):
@@ -53,6 +56,12 @@ class pkm_norm_shape(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("d", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
                 ("add_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32),
                 ("grad_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class pkm_linear_shape(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("activation", ctypes.c_int32)]
 
 
 class pkm_adamw_tensor(ctypes.Structure):
@@ -118,6 +127,13 @@ def lib() -> ctypes.CDLL:
         L.pkm_layernorm_forward.restype = ctypes.c_int
         L.pkm_layernorm_backward.argtypes = [N] + [P] * 10 + [ctypes.c_size_t, P]
         L.pkm_layernorm_backward.restype = ctypes.c_int
+        D = ctypes.POINTER(pkm_linear_shape)
+        L.pkm_linear_workspace_size.argtypes = [D, ctypes.c_int]
+        L.pkm_linear_workspace_size.restype = ctypes.c_size_t
+        L.pkm_linear_forward.argtypes = [D] + [P] * 7 + [ctypes.c_size_t, P]
+        L.pkm_linear_forward.restype = ctypes.c_int
+        L.pkm_linear_backward.argtypes = [D] + [P] * 8 + [ctypes.c_size_t, P]
+        L.pkm_linear_backward.restype = ctypes.c_int
         L.pkm_adamw_step.argtypes = [ctypes.POINTER(pkm_adamw_tensor), ctypes.c_int64,
                                      ctypes.POINTER(pkm_adamw_hyper), P, P]
         L.pkm_adamw_step.restype = ctypes.c_int
@@ -566,11 +582,11 @@ def pkm_layernorm_backward(grad_y: torch.Tensor, x: torch.Tensor, mean: torch.Te
         if workspace is None:
             n = int(lib().pkm_norm_workspace_size(ctypes.byref(shape)))
             workspace = c.empty(max(n, 1), torch.uint8)
+        ws, nbytes = _given_workspace(c, workspace)
         rc = lib().pkm_layernorm_backward(ctypes.byref(shape), _addr(grad_y), _addr(x),
                                           _addr(mean), _addr(rstd), _addr(gamma), _addr(grad_sum),
                                           _addr(grad_x), _addr(grad_gamma), _addr(grad_beta),
-                                          _ptr(workspace),
-                                          workspace.numel() * workspace.element_size(), c.handle)
+                                          _addr(ws), nbytes, c.handle)
     if rc != PKM_OK:
         raise PKMError("pkm_layernorm_backward", rc)
     return grad_x, grad_gamma, grad_beta
@@ -670,3 +686,123 @@ def pkm_adamw_step(tensors: AdamWTensors, lr: float, step: int, betas=(0.9, 0.99
                                   c.handle)
     if rc != PKM_OK:
         raise PKMError("pkm_adamw_step", rc)
+
+
+def _activation(name) -> int:
+    if isinstance(name, int):
+        return name
+    if name not in _ACTS:
+        raise ValueError("activation is one of %s" % ", ".join(sorted(_ACTS)))
+    return _ACTS[name]
+
+
+def make_linear_shape(M, N, K, dtype, out_dtype=None, activation="none") -> pkm_linear_shape:
+    """Sizes of a dense layer: x [M][K], W [N][K] of dtype, y (in the backward grad_x) of
+    out_dtype (dtype by default)."""
+    return pkm_linear_shape(int(M), int(N), int(K), _dtype(dtype),
+                            _dtype(dtype if out_dtype is None else out_dtype),
+                            _activation(activation))
+
+
+def alloc_linear_workspace(shape: pkm_linear_shape, for_backward: bool = False,
+                           device=None) -> torch.Tensor:
+    n = int(lib().pkm_linear_workspace_size(ctypes.byref(shape), int(bool(for_backward))))
+    if n == 0:
+        raise PKMError("pkm_linear_workspace_size", -1)
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def _given_workspace(c: _Call, workspace: torch.Tensor):
+    if not workspace.is_contiguous() or workspace.device != c.device:
+        raise ValueError("workspace must be contiguous and on %s" % c.device)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _linear_workspace(c: _Call, shape: pkm_linear_shape, workspace, for_backward: int):
+    """(workspace, bytes): the caller's, or one for this call."""
+    if workspace is None:
+        n = int(lib().pkm_linear_workspace_size(ctypes.byref(shape), for_backward))
+        return c.empty(max(n, 1), torch.uint8), n
+    return _given_workspace(c, workspace)
+
+
+def _linear_operands(x: torch.Tensor, W: torch.Tensor):
+    if x.dim() != 2 or W.dim() != 2:
+        raise ValueError("x must be [M][K] and W [N][K]")
+    (M, K), N, dev = x.shape, W.shape[0], x.device
+    _check("x", x, (M, K), None, dev)
+    _check("W", W, (N, K), x.dtype, dev)
+    return M, N, K, dev
+
+
+def pkm_linear_forward(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                       residual: Optional[torch.Tensor] = None, activation: str = "none",
+                       out_dtype: Optional[torch.dtype] = None, want_pre: bool = False,
+                       out: Optional[torch.Tensor] = None, pre: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None):
+    """Dense layer: (y, pre) with pre = x W^T + bias and y = activation(pre) + residual.
+
+    x [M][K] and W [N][K] both fp32 or both bf16, bias [N] fp32, activation "none", "relu",
+    "gelu" (exact) or "silu". y and residual [M][N] have type out_dtype (x's by default);
+    residual may be out itself. pre [M][N] of x's type is what pkm_linear_backward takes
+    (None unless given or want_pre)."""
+    M, N, K, dev = _linear_operands(x, W)
+    act = _activation(activation)
+    if bias is not None:
+        _check("bias", bias, (N,), torch.float32, dev)
+    if out is not None:
+        _check("out", out, (M, N), out_dtype, dev)
+        out_dtype = out.dtype
+    if residual is not None:
+        _check("residual", residual, (M, N), out_dtype, dev)
+        out_dtype = residual.dtype
+    out_dtype = out_dtype or x.dtype
+    if pre is not None:
+        _check("pre", pre, (M, N), x.dtype, dev)
+    shape = make_linear_shape(M, N, K, x.dtype, out_dtype, act)
+    with _Call(dev, stream) as c:
+        if out is None:
+            out = c.empty((M, N), out_dtype)
+        if pre is None and want_pre:
+            pre = c.empty((M, N), x.dtype)
+        ws, nbytes = _linear_workspace(c, shape, workspace, 0)
+        rc = lib().pkm_linear_forward(ctypes.byref(shape), _addr(x), _addr(W), _addr(bias),
+                                      _addr(residual), _addr(out), _addr(pre),
+                                      _addr(ws), nbytes, c.handle)
+    if rc != PKM_OK:
+        raise PKMError("pkm_linear_forward", rc)
+    return out, pre
+
+
+def pkm_linear_backward(x: torch.Tensor, W: torch.Tensor, grad_y: torch.Tensor, grads: dict,
+                        pre: Optional[torch.Tensor] = None, activation: str = "none",
+                        workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Backward of pkm_linear_forward.
+
+    ``grads`` maps any of x [M][K] (fp32 or bf16), W [N][K] fp32 and bias [N] fp32 to device
+    tensors, overwritten; missing entries are not computed. grad_y [M][N] has x's type, and
+    so has pre, the forward's (needed with an activation). The residual's gradient is grad_y."""
+    M, N, K, dev = _linear_operands(x, W)
+    act = _activation(activation)
+    _check("grad_y", grad_y, (M, N), x.dtype, dev)
+    if pre is not None:
+        _check("pre", pre, (M, N), x.dtype, dev)
+    unknown = set(grads) - {"x", "W", "bias"}
+    if unknown:
+        raise ValueError("grads takes x, W and bias, not %s" % ", ".join(sorted(unknown)))
+    gx, gW, gb = (grads.get(k) for k in ("x", "W", "bias"))
+    if gx is not None:
+        _check("grads['x']", gx, (M, K), None, dev)
+    if gW is not None:
+        _check("grads['W']", gW, (N, K), torch.float32, dev)
+    if gb is not None:
+        _check("grads['bias']", gb, (N,), torch.float32, dev)
+    shape = make_linear_shape(M, N, K, x.dtype, x.dtype if gx is None else gx.dtype, act)
+    with _Call(dev, stream) as c:
+        ws, nbytes = _linear_workspace(c, shape, workspace, 1)
+        rc = lib().pkm_linear_backward(ctypes.byref(shape), _addr(x), _addr(W), _addr(grad_y),
+                                       _addr(pre), _addr(gx), _addr(gW), _addr(gb),
+                                       _addr(ws), nbytes, c.handle)
+    if rc != PKM_OK:
+        raise PKMError("pkm_linear_backward", rc)
+    return grads

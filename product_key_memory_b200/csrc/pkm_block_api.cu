@@ -7,6 +7,7 @@
 
 #include "../../include/pkm.h"
 #include "pkm_block.h"
+#include "pkm_linear.h"
 
 namespace {
 
@@ -49,6 +50,20 @@ int validate_norm(const pkm_norm_shape* s, bool has_add) {
 
 pkm::NormArgs norm_args(const pkm_norm_shape* s) {
   return {s->rows, s->d, s->x_dtype, s->add_dtype, s->y_dtype, s->grad_dtype, s->eps};
+}
+
+int validate_linear(const pkm_linear_shape* s) {
+  if (!s || s->M < 0 || s->N < 1 || s->K < 1 || !is_dtype(s->dtype) || !is_dtype(s->out_dtype) ||
+      s->activation < PKM_ACT_NONE || s->activation > PKM_ACT_SILU)
+    return PKM_ERR_INVALID_ARG;
+  const int64_t wide = s->N > s->K ? s->N : s->K;
+  if (s->M > 0x7fffffffLL - 256 || wide > pkm::kLinearMaxWidth || s->M * wide >= 1LL << 38)
+    return PKM_ERR_UNSUPPORTED;
+  return PKM_OK;
+}
+
+pkm::LinearArgs linear_args(const pkm_linear_shape* s) {
+  return {s->M, s->N, s->K, s->dtype, s->out_dtype, s->activation};
 }
 
 }  // namespace
@@ -101,6 +116,57 @@ int pkm_layernorm_backward(const pkm_norm_shape* s, const void* grad_y, const vo
                                                grad_sum, grad_x, grad_gamma, grad_beta,
                                                static_cast<float*>(workspace), st),
                 grad_gamma || grad_beta ? 2 : 1);
+}
+
+size_t pkm_linear_workspace_size(const pkm_linear_shape* s, int for_backward) {
+  if (validate_linear(s) != PKM_OK) return 0;
+  return pkm::linear_workspace_bytes(linear_args(s), for_backward != 0);
+}
+
+int pkm_linear_forward(const pkm_linear_shape* s, const void* x, const void* W, const float* bias,
+                       const void* residual, void* y, void* pre, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  const int rc = validate_linear(s);
+  if (rc != PKM_OK) return rc;
+  if (!W || (s->M > 0 && (!x || !y))) return PKM_ERR_INVALID_ARG;
+  if (!all_aligned16({x, W, bias, residual, y, pre})) return PKM_ERR_UNSUPPORTED;
+  const pkm::LinearArgs a = linear_args(s);
+  if (!workspace || workspace_bytes < pkm::linear_workspace_bytes(a, false) ||
+      !aligned256(workspace))
+    return PKM_ERR_WORKSPACE;
+  if (s->M == 0) return PKM_OK;
+  const Range range("pkm.linear_forward");
+  int launches = 0;
+  const cudaError_t e = pkm::launch_linear_forward(a, x, W, bias, residual, y, pre, workspace,
+                                                   &launches, static_cast<cudaStream_t>(stream));
+  return finish(e, launches);
+}
+
+int pkm_linear_backward(const pkm_linear_shape* s, const void* x, const void* W,
+                        const void* grad_y, const void* pre, void* grad_x, float* grad_W,
+                        float* grad_bias, void* workspace, size_t workspace_bytes, void* stream) {
+  const int rc = validate_linear(s);
+  if (rc != PKM_OK) return rc;
+  const bool act = s->activation != PKM_ACT_NONE;
+  if (!W || (s->M > 0 && (!x || !grad_y || (act && !pre)))) return PKM_ERR_INVALID_ARG;
+  if (!all_aligned16({x, W, grad_y, pre, grad_x, grad_W, grad_bias})) return PKM_ERR_UNSUPPORTED;
+  const pkm::LinearArgs a = linear_args(s);
+  if (!workspace || workspace_bytes < pkm::linear_workspace_bytes(a, true) ||
+      !aligned256(workspace))
+    return PKM_ERR_WORKSPACE;
+  const Range range("pkm.linear_backward");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (s->M == 0) {
+    if (grad_W && cudaMemsetAsync(grad_W, 0, sizeof(float) * s->N * s->K, st) != cudaSuccess)
+      return PKM_ERR_CUDA;
+    if (grad_bias && cudaMemsetAsync(grad_bias, 0, sizeof(float) * s->N, st) != cudaSuccess)
+      return PKM_ERR_CUDA;
+    return PKM_OK;
+  }
+  int launches = 0;
+  const cudaError_t e = pkm::launch_linear_backward(a, x, W, grad_y, pre, grad_x, grad_W,
+                                                    grad_bias, workspace, &launches, st);
+  return finish(e, launches);
 }
 
 int pkm_adamw_step(const pkm_adamw_tensor* tensors, int64_t count, const pkm_adamw_hyper* h,

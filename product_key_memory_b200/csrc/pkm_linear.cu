@@ -1,0 +1,489 @@
+// pkm_linear.cu -- the dense layer around its tensor-core product: the small-batch
+// forward, operand planes, the backward's d = grad_y act'(pre), column sums, and the sum
+// of a split product.
+#include "pkm_linear.h"
+
+#include "pkm_block.h"
+#include "pkm_linear_epi.cuh"
+#include "pkm_tc.h"
+#include "pkm_tcgen05.cuh"
+
+namespace pkm {
+
+namespace {
+
+constexpr int kSmallM = 8;          // rows of the small-batch kernel
+constexpr int kMaxSplit = 16;
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+int64_t pad8(int64_t x) { return (x + 7) / 8 * 8; }
+
+// ---------------------------------------------------------------- small batches
+// One warp per output column: the lanes split the W row (read once, 4 accesses in flight),
+// x comes from L1/L2, the lanes' sums are added by a tree. Bound by reading W.
+template <typename E, int V, int M>
+__global__ void __launch_bounds__(256) linear_small_kernel(const void* x, const void* W, int N,
+                                                           int K, const LinearEpilogue epi) {
+  const int lane = threadIdx.x & 31;
+  const int col = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (col >= N) return;
+  const int64_t base = static_cast<int64_t>(col) * K;
+  float acc[M] = {};
+  constexpr int kDepth = 4;
+  for (int k0 = lane * V; k0 < K; k0 += 32 * V * kDepth) {
+    Raw<E, V> w[kDepth];
+#pragma unroll
+    for (int u = 0; u < kDepth; ++u)
+      if (k0 + u * 32 * V < K) w[u].load(W, base + k0 + u * 32 * V);
+#pragma unroll
+    for (int u = 0; u < kDepth; ++u) {
+      const int k = k0 + u * 32 * V;
+      if (k >= K) break;
+      float wf[V];
+      w[u].get(wf);
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        Raw<E, V> xr;
+        float xf[V];
+        xr.load(x, static_cast<int64_t>(m) * K + k);
+        xr.get(xf);
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[m] = fmaf(wf[v], xf[v], acc[m]);
+      }
+    }
+  }
+  float mine = 0.f;
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    const float s = warp_sum(acc[m]);
+    if (lane == m) mine = s;
+  }
+  if (lane < M) linear_store1(epi, static_cast<int64_t>(lane) * N + col, col, mine);
+}
+
+template <typename E, int V>
+cudaError_t run_small(int M, const void* x, const void* W, int N, int K,
+                      const LinearEpilogue& epi, cudaStream_t st) {
+  const unsigned grid = static_cast<unsigned>((N + 7) / 8);
+  switch (M) {
+#define PKM_CASE(m) \
+  case m: linear_small_kernel<E, V, m><<<grid, 256, 0, st>>>(x, W, N, K, epi); break;
+    PKM_CASE(1) PKM_CASE(2) PKM_CASE(3) PKM_CASE(4) PKM_CASE(5) PKM_CASE(6) PKM_CASE(7)
+    default: linear_small_kernel<E, V, 8><<<grid, 256, 0, st>>>(x, W, N, K, epi);
+#undef PKM_CASE
+  }
+  return cudaGetLastError();
+}
+
+// --------------------------------------------------------------- operand planes
+// v as bf16 planes hi, mid, lo (rounded to nearest, so the sum is v to 2^-24); a value
+// that hi cannot hold as finite leaves zeros below it.
+__device__ __forceinline__ void split(float v, float* p) {
+  p[0] = rounded<BF16>(v);
+  const bool fine = fabsf(p[0]) < __uint_as_float(0x7f800000u);
+  p[1] = fine ? rounded<BF16>(v - p[0]) : 0.f;
+  p[2] = fine ? rounded<BF16>(v - p[0] - p[1]) : 0.f;
+}
+
+template <typename E, int V>
+__device__ __forceinline__ void load_cols(const void* p, int64_t at, int col, int cols, float* f) {
+  if (V == 8) {
+    Raw<E, 8> r;
+    r.load(p, at);
+    r.get(f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      f[j] = 0.f;
+      if (col + j < cols) {
+        Raw<E, 1> r;
+        r.load(p, at + j);
+        r.get(f + j);
+      }
+    }
+  }
+}
+
+template <int NP>
+__device__ __forceinline__ void store_planes(uint16_t* dst, int64_t plane, int64_t at,
+                                             const float* f) {
+  float p[3][8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float q[3];
+    if (NP == 1) {
+      q[0] = f[j];
+    } else {
+      split(f[j], q);
+    }
+#pragma unroll
+    for (int n = 0; n < NP; ++n) p[n][j] = q[n];
+  }
+#pragma unroll
+  for (int n = 0; n < NP; ++n) Out<BF16, 8>::store(dst + n * plane, at, p[n]);
+}
+
+// [rows][cols] of E -> NP planes [rows][ld] of bf16, ld a multiple of 8.
+template <typename E, int V, int NP>
+__global__ void __launch_bounds__(256) linear_planes_kernel(const void* src, uint16_t* dst,
+                                                            int64_t rows, int cols, int64_t ld) {
+  const int chunks = static_cast<int>(ld / 8);
+  const int64_t total = rows * chunks;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t r = i / chunks;
+    const int col = static_cast<int>(i - r * chunks) * 8;
+    float f[8];
+    load_cols<E, V>(src, r * cols + col, col, cols, f);
+    store_planes<NP>(dst, rows * ld, r * ld + col, f);
+  }
+}
+
+cudaError_t make_planes(const void* src, int dtype, uint16_t* dst, int64_t rows, int cols,
+                        cudaStream_t st) {
+  const int64_t ld = pad8(cols);
+  const int64_t blocks = (rows * (ld / 8) + 255) / 256;
+  const unsigned grid = static_cast<unsigned>(blocks < 148 * 32 ? blocks : 148 * 32);
+  const bool vec = cols % 8 == 0;
+  if (dtype == PKM_F32) {
+    if (vec) linear_planes_kernel<F32, 8, 3><<<grid, 256, 0, st>>>(src, dst, rows, cols, ld);
+    else linear_planes_kernel<F32, 1, 3><<<grid, 256, 0, st>>>(src, dst, rows, cols, ld);
+  } else {
+    linear_planes_kernel<BF16, 1, 1><<<grid, 256, 0, st>>>(src, dst, rows, cols, ld);
+  }
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------ d = grad_y act'(pre)
+// Block: 256 columns (32 lanes of 8) x kPrepRows rows (8 warps, every eighth row each). d is
+// written as NP planes (NP = 0: not needed) and its column sums as one partial row per block
+// row (part NULL: not needed).
+constexpr int kPrepRows = 64;
+
+template <typename E, int V, int NP>
+__global__ void __launch_bounds__(256) linear_slope_kernel(const void* gy, const void* pre,
+                                                           int act, uint16_t* dst, float* part,
+                                                           int64_t rows, int cols, int64_t ld) {
+  __shared__ float sh[8][256];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = blockIdx.y * 256 + lane * 8;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kPrepRows;
+  float sum[8] = {};
+  if (col < cols) {
+    const int64_t r1 = r0 + kPrepRows < rows ? r0 + kPrepRows : rows;
+    for (int64_t r = r0 + warp; r < r1; r += 8) {
+      float g[8];
+      load_cols<E, V>(gy, r * cols + col, col, cols, g);
+      if (act != PKM_ACT_NONE) {
+        float t[8];
+        load_cols<E, V>(pre, r * cols + col, col, cols, t);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] *= act_slope(t[j], act);
+      }
+      if (NP > 0) store_planes<NP>(dst, rows * ld, r * ld + col, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += g[j];
+    }
+  }
+  if (!part) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sh[warp][lane * 8 + j] = sum[j];
+  __syncthreads();
+  const int c = blockIdx.y * 256 + threadIdx.x;
+  if (c < cols) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) s += sh[w][threadIdx.x];
+    part[static_cast<int64_t>(blockIdx.x) * cols + c] = s;
+  }
+}
+
+__global__ void __launch_bounds__(256) linear_bias_kernel(const float* __restrict__ part, int64_t blocks,
+                                                          int cols, float* out) {
+  __shared__ float sh[8][33];
+  const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + c;
+  float s = 0.f;
+  if (col < cols)
+    for (int64_t r = k; r < blocks; r += 8) s += part[r * cols + col];
+  sh[k][c] = s;
+  __syncthreads();
+  if (k == 0 && col < cols) {
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a += sh[i][c];
+    out[col] = a;
+  }
+}
+
+template <typename E, int V>
+cudaError_t run_slope(int planes, const void* gy, const void* pre, int act, uint16_t* dst,
+                      float* part, int64_t rows, int cols, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>((rows + kPrepRows - 1) / kPrepRows),
+                  static_cast<unsigned>((cols + 255) / 256));
+  const int64_t ld = pad8(cols);
+  switch (planes) {
+    case 0:
+      linear_slope_kernel<E, V, 0><<<grid, 256, 0, st>>>(gy, pre, act, dst, part, rows, cols, ld);
+      break;
+    case 1:
+      linear_slope_kernel<E, V, 1><<<grid, 256, 0, st>>>(gy, pre, act, dst, part, rows, cols, ld);
+      break;
+    case 2:
+      linear_slope_kernel<E, V, 2><<<grid, 256, 0, st>>>(gy, pre, act, dst, part, rows, cols, ld);
+      break;
+    default:
+      linear_slope_kernel<E, V, 3><<<grid, 256, 0, st>>>(gy, pre, act, dst, part, rows, cols, ld);
+  }
+  return cudaGetLastError();
+}
+
+// ----------------------------------------------------------------- split products
+// Adds the `splits` parts of each element in order and applies the epilogue: a thread takes
+// four columns of a row.
+__global__ void __launch_bounds__(256) linear_finish_kernel(LinearEpilogue epi, int64_t M, int N,
+                                                            int splits) {
+  const float* part = epi.part;
+  const int quads = static_cast<int>(epi.ldp / 4);
+  const int64_t total = M * quads;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= total) return;
+  const int64_t r = i / quads;
+  const int col = static_cast<int>(i - r * quads) * 4;
+  float4 s = *reinterpret_cast<const float4*>(part + r * epi.ldp + col);
+  for (int k = 1; k < splits; ++k) {
+    const float4 t = *reinterpret_cast<const float4*>(part + (k * M + r) * epi.ldp + col);
+    s.x += t.x; s.y += t.y; s.z += t.z; s.w += t.w;
+  }
+  const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (col + j < N) linear_store1(epi, r * N + col + j, col + j, v[j]);
+}
+
+// ------------------------------------------------------------------- host side
+// A product's tile and split. The pair tile reads a third less per product than the single
+// ones, so it is taken where it fills the SMs; else the largest tile that does, and where
+// none does, the smallest with K split over the idle SMs.
+struct Plan {
+  LinearTile tile;
+  int ksplit;
+};
+
+Plan plan_gemm(int64_t M, int64_t N, int64_t steps) {
+  const auto tiles = [&](int rows, int cols) {
+    return ((M + rows - 1) / rows) * ((N + cols - 1) / cols);
+  };
+  const int sms = 148;   // the workspace's size depends on the plan, so on sizes alone
+  if (tiles(256, 256) * 2 >= sms * 3 / 4) return {kTile256, 1};
+  if (tiles(128, 128) >= sms * 3 / 4) return {kTile128, 1};
+  const int64_t t = tiles(128, 64);
+  int64_t split = sms / t;
+  if (split > kMaxSplit) split = kMaxSplit;
+  if (split > steps / 4) split = steps / 4;   // at least four K steps each
+  if (split <= 1) return {kTile64, 1};
+  const int64_t per = (steps + split - 1) / split;
+  return {kTile64, static_cast<int>((steps + per - 1) / per)};
+}
+
+struct PlaneSet {
+  uint32_t a, b;
+  int pairs;
+};
+
+// The plane pairs of a product: p + q below the larger plane count.
+PlaneSet plane_pairs(int a, int b) {
+  if (a == 3 && b == 3) return {0x210100u, 0x012010u, 6};
+  if (a == 2) return {0x10u, 0x00u, 2};
+  return {0u, 0u, 1};
+}
+
+int64_t k_steps(int64_t K, int pairs) { return (K + 63) / 64 * pairs; }
+
+// Number of planes of an operand of the layer's type; in place (0 bytes) for bf16 rows of
+// 16-byte multiples.
+int input_planes(int dtype) { return dtype == PKM_F32 ? 3 : 1; }
+bool in_place(int dtype, int cols) { return dtype == PKM_BF16 && cols % 8 == 0; }
+size_t planes_bytes(int dtype, int64_t rows, int cols) {
+  return in_place(dtype, cols) ? 0 : align256(static_cast<size_t>(rows) * pad8(cols) * 2 *
+                                              input_planes(dtype));
+}
+
+size_t part_bytes(const Plan& p, int64_t M, int64_t N) {
+  return p.ksplit > 1 ? align256(static_cast<size_t>(p.ksplit) * M * ((N + 3) / 4 * 4) * 4) : 0;
+}
+
+// The backward's d: planes written (0: grad_y itself is the operand).
+int slope_planes(const LinearArgs& a) {
+  if (a.dtype == PKM_F32) return 3;
+  if (a.act != PKM_ACT_NONE) return 2;
+  return a.N % 8 == 0 ? 0 : 1;
+}
+
+struct Layout {
+  size_t x, W, d, part, bias, total;   // offsets; total = bytes
+  Plan fwd, gx, gw;
+  PlaneSet fwd_p, gx_p, gw_p;
+};
+
+Layout layout(const LinearArgs& a, bool backward) {
+  Layout l{};
+  size_t off = kStatusBytes;
+  const int in = input_planes(a.dtype);
+  l.x = off;
+  off += planes_bytes(a.dtype, a.M, a.K);
+  l.W = off;
+  off += planes_bytes(a.dtype, a.N, a.K);
+  l.part = off;
+  if (!backward) {
+    l.fwd_p = plane_pairs(in, in);
+    l.fwd = plan_gemm(a.M, a.N, k_steps(a.K, l.fwd_p.pairs));
+    off += part_bytes(l.fwd, a.M, a.N);
+  } else {
+    const int d = slope_planes(a);
+    // grad_x in bf16: d's rounding to bf16 is no larger than grad_x's own, one plane will do.
+    l.gx_p = plane_pairs(d == 2 && a.out_dtype == PKM_BF16 ? 1 : (d ? d : 1), in);
+    l.gw_p = plane_pairs(d ? d : 1, in);
+    l.gx = plan_gemm(a.M, a.K, k_steps(a.N, l.gx_p.pairs));
+    l.gw = plan_gemm(a.N, a.K, k_steps(a.M, l.gw_p.pairs));
+    const size_t px = part_bytes(l.gx, a.M, a.K), pw = part_bytes(l.gw, a.N, a.K);
+    off += px > pw ? px : pw;    // the two products run one after the other
+    l.d = off;
+    off += align256(static_cast<size_t>(a.M) * pad8(a.N) * 2 * d);
+    l.bias = off;
+    off += align256(static_cast<size_t>((a.M + kPrepRows - 1) / kPrepRows) * a.N * 4);
+  }
+  l.total = off;
+  return l;
+}
+
+// A product and, when it is split, the pass that adds the parts.
+cudaError_t product(LinearGemm g, float* part, int* launches, cudaStream_t st) {
+  if (g.ksplit > 1) {
+    g.epi.part = part;
+    g.epi.ldp = (static_cast<int64_t>(g.N) + 3) / 4 * 4;
+  }
+  cudaError_t e = launch_linear_gemm(g, st);
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  if (g.ksplit == 1) return cudaSuccess;
+  const int64_t total = static_cast<int64_t>(g.M) * (g.epi.ldp / 4);
+  linear_finish_kernel<<<static_cast<unsigned>((total + 255) / 256), 256, 0, st>>>(g.epi, g.M, g.N,
+                                                                                 g.ksplit);
+  ++*launches;
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool linear_small(const LinearArgs& a) { return a.M <= kSmallM; }
+
+size_t linear_workspace_bytes(const LinearArgs& a, bool backward) {
+  if (a.M == 0 || (!backward && linear_small(a))) return kStatusBytes;
+  return layout(a, backward).total;
+}
+
+cudaError_t launch_linear_forward(const LinearArgs& a, const void* x, const void* W,
+                                  const float* bias, const void* residual, void* y, void* pre,
+                                  void* workspace, int* launches, cudaStream_t st) {
+  LinearEpilogue epi{y, bias, residual, pre, nullptr, 0, a.out_dtype == PKM_F32,
+                     a.dtype == PKM_F32, a.act};
+  int* status = static_cast<int*>(workspace);
+  cudaError_t e = cudaMemsetAsync(status, 0, sizeof(int), st);
+  if (e != cudaSuccess) return e;
+  if (linear_small(a)) {
+    ++*launches;
+    const int M = static_cast<int>(a.M);
+    const bool vec = a.K % 8 == 0;
+    if (a.dtype == PKM_F32)
+      return vec ? run_small<F32, 8>(M, x, W, a.N, a.K, epi, st)
+                 : run_small<F32, 1>(M, x, W, a.N, a.K, epi, st);
+    return vec ? run_small<BF16, 8>(M, x, W, a.N, a.K, epi, st)
+               : run_small<BF16, 1>(M, x, W, a.N, a.K, epi, st);
+  }
+  const Layout l = layout(a, false);
+  char* ws = static_cast<char*>(workspace);
+  const int64_t ld = pad8(a.K);
+  if (!in_place(a.dtype, a.K)) {
+    e = make_planes(x, a.dtype, reinterpret_cast<uint16_t*>(ws + l.x), a.M, a.K, st);
+    if (e == cudaSuccess)
+      e = make_planes(W, a.dtype, reinterpret_cast<uint16_t*>(ws + l.W), a.N, a.K, st);
+    if (e != cudaSuccess) return e;
+    x = ws + l.x;
+    W = ws + l.W;
+    *launches += 2;
+  }
+  const uint32_t in = static_cast<uint32_t>(input_planes(a.dtype));
+  const LinearGemm g{kForward, l.fwd.tile, x, W, ld, ld, static_cast<int>(a.M), a.N, a.K, in, in,
+                     l.fwd_p.a, l.fwd_p.b, l.fwd_p.pairs, l.fwd.ksplit, epi, status};
+  return product(g, reinterpret_cast<float*>(ws + l.part), launches, st);
+}
+
+cudaError_t launch_linear_backward(const LinearArgs& a, const void* x, const void* W,
+                                   const void* grad_y, const void* pre, void* grad_x,
+                                   float* grad_W, float* grad_bias, void* workspace,
+                                   int* launches, cudaStream_t st) {
+  const Layout l = layout(a, true);
+  char* ws = static_cast<char*>(workspace);
+  int* status = static_cast<int*>(workspace);
+  cudaError_t e = cudaMemsetAsync(status, 0, sizeof(int), st);
+  if (e != cudaSuccess) return e;
+  const int dp = slope_planes(a);
+  const int64_t ldn = pad8(a.N), ldk = pad8(a.K);
+  uint16_t* d = reinterpret_cast<uint16_t*>(ws + l.d);
+  const bool want_d = grad_x || grad_W;
+  if (grad_bias || (want_d && dp > 0)) {
+    float* part = grad_bias ? reinterpret_cast<float*>(ws + l.bias) : nullptr;
+    const int planes = want_d ? dp : 0;
+    const bool vec = a.N % 8 == 0;
+    if (a.dtype == PKM_F32)
+      e = vec ? run_slope<F32, 8>(planes, grad_y, pre, a.act, d, part, a.M, a.N, st)
+              : run_slope<F32, 1>(planes, grad_y, pre, a.act, d, part, a.M, a.N, st);
+    else
+      e = vec ? run_slope<BF16, 8>(planes, grad_y, pre, a.act, d, part, a.M, a.N, st)
+              : run_slope<BF16, 1>(planes, grad_y, pre, a.act, d, part, a.M, a.N, st);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+    if (grad_bias) {
+      linear_bias_kernel<<<(a.N + 31) / 32, 256, 0, st>>>(
+          part, (a.M + kPrepRows - 1) / kPrepRows, a.N, grad_bias);
+      e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+      ++*launches;
+    }
+  }
+  if (!want_d) return cudaSuccess;
+  const void* dop = dp ? static_cast<const void*>(d) : grad_y;
+  const uint32_t dcount = dp ? dp : 1, in = static_cast<uint32_t>(input_planes(a.dtype));
+  const bool inpl = in_place(a.dtype, a.K);
+  float* part = reinterpret_cast<float*>(ws + l.part);
+  if (grad_x) {
+    if (!inpl) {
+      e = make_planes(W, a.dtype, reinterpret_cast<uint16_t*>(ws + l.W), a.N, a.K, st);
+      if (e != cudaSuccess) return e;
+      W = ws + l.W;
+      ++*launches;
+    }
+    const LinearEpilogue epi{grad_x, nullptr, nullptr, nullptr, nullptr, 0,
+                             a.out_dtype == PKM_F32, 0, PKM_ACT_NONE};
+    const LinearGemm g{kGradX, l.gx.tile, dop, W, ldn, ldk, static_cast<int>(a.M), a.K, a.N,
+                       dcount, in, l.gx_p.a, l.gx_p.b, l.gx_p.pairs, l.gx.ksplit, epi, status};
+    e = product(g, part, launches, st);
+    if (e != cudaSuccess) return e;
+  }
+  if (grad_W) {
+    if (!inpl) {
+      e = make_planes(x, a.dtype, reinterpret_cast<uint16_t*>(ws + l.x), a.M, a.K, st);
+      if (e != cudaSuccess) return e;
+      x = ws + l.x;
+      ++*launches;
+    }
+    const LinearEpilogue epi{grad_W, nullptr, nullptr, nullptr, nullptr, 0, 1, 0, PKM_ACT_NONE};
+    const LinearGemm g{kGradW, l.gw.tile, dop, x, ldn, ldk, a.N, a.K, static_cast<int>(a.M),
+                       dcount, in, l.gw_p.a, l.gw_p.b, l.gw_p.pairs, l.gw.ksplit, epi, status};
+    e = product(g, part, launches, st);
+  }
+  return e;
+}
+
+}  // namespace pkm

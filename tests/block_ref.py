@@ -130,3 +130,26 @@ def adamw(t, hyper, index):
     near = ((near / ulp).round() * ulp).clamp(min=2.0 ** -9)
     out["v"] = torch.where(q > 0, near.float(), q).to(torch.float8_e4m3fn)
     return out
+
+
+# ------------------------------------------------------------------------------- dense layer
+def act(t, name):
+    if name == "relu":
+        return torch.where(t <= 0, torch.zeros_like(t), t)
+    if name == "gelu":
+        return 0.5 * t * torch.special.erfc(-t * 0.5 ** 0.5)
+    if name == "silu":
+        return t * torch.sigmoid(t)
+    return t
+
+
+def act_slope(t, name):
+    if name == "relu":
+        return (t > 0).to(t.dtype)
+    if name == "gelu":
+        return 0.5 * torch.special.erfc(-t * 0.5 ** 0.5) + \
+            t * torch.exp(-0.5 * t * t) * 0.3989422804014327
+    if name == "silu":
+        s = torch.sigmoid(t)
+        return s * (1 + t * (1 - s))
+    return torch.ones_like(t)

@@ -136,3 +136,86 @@ def test_adamw_binding_checks_tensors():
         P.alloc_adamw_state(x, 16)
     s = P.alloc_adamw_state(torch.zeros(300), 8)
     assert s["m"].dtype == torch.float8_e4m3fn and s["v_scale"].shape == (2,)
+
+
+def _linear(**kw):
+    base = dict(M=100, N=72, K=80, dtype=1, out_dtype=1, activation=0)
+    base.update(kw)
+    return P.pkm_linear_shape(**base)
+
+
+def _linear_forward(s, ws=OK, nbytes=1 << 60, **kw):
+    a = dict(x=OK, W=OK, bias=None, residual=None, y=OK, pre=None)
+    a.update(kw)
+    return P.lib().pkm_linear_forward(ctypes.byref(s) if s else None, *a.values(), ws, nbytes, None)
+
+
+def _linear_backward(s, ws=OK, nbytes=1 << 60, **kw):
+    a = dict(x=OK, W=OK, gy=OK, pre=None, gx=OK, gW=OK, gb=OK)
+    a.update(kw)
+    return P.lib().pkm_linear_backward(ctypes.byref(s) if s else None, *a.values(), ws, nbytes,
+                                       None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(M=-1), -1), (dict(N=0), -1), (dict(K=0), -1), (dict(K=-8), -1), (dict(dtype=2), -1),
+    (dict(out_dtype=-1), -1), (dict(activation=4), -1), (dict(activation=-1), -1),
+    (dict(M=(1 << 31) - 1), -2), (dict(N=(1 << 20) + 1), -2), (dict(K=(1 << 20) + 1), -2),
+    (dict(M=1 << 20, N=1 << 18), -2), (dict(M=1 << 20, K=1 << 18), -2)])
+def test_linear_sizes_refused(kw, code):
+    s = _linear(**kw)
+    assert P.lib().pkm_linear_workspace_size(ctypes.byref(s), 0) == 0
+    assert P.lib().pkm_linear_workspace_size(ctypes.byref(s), 1) == 0
+    assert _linear_forward(s) == code and _linear_backward(s, pre=OK) == code
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_linear_arguments_refused(dtype):
+    s = _linear(dtype=dtype)
+    assert _linear_forward(None) == -1 and _linear_backward(None) == -1
+    for name in ("x", "W", "y"):
+        assert _linear_forward(s, **{name: None}) == -1, name
+    for name in ("x", "W", "gy"):
+        assert _linear_backward(s, **{name: None}) == -1, name
+    assert _linear_backward(_linear(dtype=dtype, activation=2)) == -1       # pre is missing
+    for name in ("x", "W", "bias", "residual", "y", "pre"):
+        assert _linear_forward(s, **{name: ODD}) == -2, name
+    for name in ("x", "W", "gy", "pre", "gx", "gW", "gb"):
+        assert _linear_backward(s, **{name: ODD}) == -2, name
+    for back, call in ((0, _linear_forward), (1, _linear_backward)):
+        need = int(P.lib().pkm_linear_workspace_size(ctypes.byref(s), back))
+        assert need >= 256
+        assert call(s, nbytes=need - 1) == -3 and call(s, ws=None) == -3
+        assert call(s, ws=ctypes.c_void_p((1 << 20) + 128)) == -3
+
+
+def test_linear_no_rows_returns_without_a_gpu():
+    s = _linear(M=0, activation=2)
+    for back in (0, 1):
+        assert P.lib().pkm_linear_workspace_size(ctypes.byref(s), back) == 256
+    assert _linear_forward(s, x=None, y=None) == 0
+    assert _linear_backward(s, x=None, gy=None, gx=None, gW=None, gb=None) == 0
+
+
+def test_linear_workspace_holds_the_planes():
+    """fp32 operands: three bf16 planes each, rows padded to 8; bf16 rows of 16-byte multiples are
+    used in place."""
+    def size(back, **kw):
+        return int(P.lib().pkm_linear_workspace_size(ctypes.byref(_linear(**kw)), back))
+    big = dict(M=4096, N=4096, K=1024)
+    assert size(0, **big) == 256
+    assert size(0, dtype=0, **big) == 256 + 3 * 2 * (4096 + 4096) * 1024
+    assert size(0, M=4096, N=4096, K=1001) == 256 + 2 * (4096 + 4096) * 1008
+    assert size(1, activation=2, **big) >= 2 * 2 * 4096 * 4096
+
+
+def test_linear_binding_checks_tensors():
+    x, W = torch.zeros(4, 8), torch.zeros(3, 8)
+    for call in (lambda: P.pkm_linear_forward(x, W), lambda: P.pkm_linear_forward(x, W[0]),
+                 lambda: P.pkm_linear_forward(x, W, activation="tanh"),
+                 lambda: P.pkm_linear_backward(x, W, torch.zeros(4, 3), {}),
+                 lambda: P.make_linear_shape(4, 3, 8, torch.float16)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(P.PKMError):
+        P.alloc_linear_workspace(P.make_linear_shape(4, 0, 8, torch.bfloat16))

@@ -1,0 +1,282 @@
+"""The dense layer and its backward on the GPU against a plain 64-bit implementation, element by
+element.
+
+A product of K terms accumulates in fp32, 16 terms a step: each step may cut the running sum to
+24 bits (2^-23 of its size, which is at most S = sum |a b|), with `pairs` steps for each 16 terms
+where operands are planes (6 in fp32 layers, 2 for a backward with an activation), and at most 16
+parts are added at the end. Planes: an fp32 value is its three planes to 2^-24, and the
+products left out, mid lo, lo mid and lo lo, are at most 2 * 2^-25 + 2^-32 of S; two planes
+are the value to 2^-17 (2^-9 of 2^-9, and 2^-1 of reserve). So
+  |err of a product| <= E = S (2^-23 (pairs K / 16 + 16) + cut),  cut = 2^-22 or 2^-17 or 0.
+Activations have slopes below 1.13 in size, second derivatives below 0.8, and cost at most 8
+roundings of their result and argument; bias, residual and the output round once each.
+"""
+import pytest
+import torch
+
+from block_ref import (BF16, F32, U, act, act_slope, assert_within, guarded, half_step)
+
+pytestmark = pytest.mark.gpu
+ACTS = ["none", "relu", "gelu", "silu"]
+
+
+def _product_bound(S, K, pairs, cut):
+    return S * (2.0 ** -23 * (pairs * K / 16 + 16) + cut)
+
+
+def _data(M, N, K, kind, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed + 7 * M + 3 * N + K)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    return rn(M, K).to(kind), (rn(N, K) * K ** -0.5).to(kind), rn
+
+
+def _check_forward(x, W, bias, residual, name, y, pre):
+    f32 = x.dtype == F32
+    K = x.shape[1]
+    xd, wd = x.double(), W.double()
+    rpre = xd @ wd.t()
+    bound = _product_bound(xd.abs() @ wd.abs().t(), K, 6 if f32 else 1, 2.0 ** -22 if f32 else 0)
+    if bias is not None:
+        rpre = rpre + bias.double()
+        bound = bound + U * rpre.abs()
+    if pre is not None:
+        assert pre.dtype == x.dtype
+        assert_within("pre", pre, rpre, bound + half_step(x.dtype) * (rpre.abs() + bound))
+    ry = act(rpre, name)
+    b = 1.13 * bound
+    if name == "relu":
+        b = bound
+    if name in ("gelu", "silu"):
+        b = b + 8 * U * (ry.abs() + rpre.abs() * 0.5 * (rpre.abs() < 12))
+    if residual is not None:
+        ry = ry + residual.double()
+        b = b + U * ry.abs()
+    assert_within("y", y, ry, b + half_step(y.dtype) * (ry.abs() + b))
+
+
+# (M, N, K): single rows and small batches, odd sizes, one of each tile and split, widths of one.
+SIZES = [(1, 1, 1), (1, 4096, 1024), (2, 33, 65), (3, 100, 1000), (5, 7, 24), (8, 515, 1001),
+         (9, 64, 64), (9, 1, 3000), (16, 130, 72), (33, 515, 1001), (64, 4096, 1024), (129, 257, 8),
+         (128, 64, 6400), (300, 1600, 264), (777, 515, 1001), (1500, 1536, 136), (2048, 2048, 192),
+         (2100, 2056, 200), (2049, 2305, 77)]
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+@pytest.mark.parametrize("kind", [BF16, F32])
+def test_forward_sizes(M, N, K, kind):
+    import product_key_memory_b200 as P
+    x, W, rn = _data(M, N, K, kind)
+    i = M + N + K + (kind == F32)
+    name = ACTS[i % 4]
+    yt = F32 if i % 3 == 0 else kind
+    bias = rn(N) if i % 2 else None
+    residual = rn(M, N).to(yt) if i % 5 < 3 else None
+    out, check_out = guarded((M, N), yt)
+    pre, check_pre = guarded((M, N), kind)
+    shape = P.make_linear_shape(M, N, K, kind, yt, name)
+    ws = P.alloc_linear_workspace(shape, False, "cuda").fill_(255)
+    P.pkm_linear_forward(x, W, bias, residual, name, out=out, pre=pre, workspace=ws)
+    assert P.pkm_device_status(ws) == 0
+    _check_forward(x, W, bias, residual, name, out, pre)
+    check_out()
+    check_pre()
+
+
+@pytest.mark.parametrize("kind", [BF16, F32])
+@pytest.mark.parametrize("yt", [BF16, F32])
+@pytest.mark.parametrize("name", ACTS)
+def test_forward_types_and_activations(kind, yt, name):
+    import product_key_memory_b200 as P
+    for M, N, K in ((4, 72, 80), (40, 72, 80), (200, 131, 96)):
+        x, W, rn = _data(M, N, K, kind, seed=5)
+        x = x * 3
+        bias, residual = rn(N), rn(M, N).to(yt)
+        y, pre = P.pkm_linear_forward(x, W, bias, residual, name, want_pre=M != 40)
+        assert y.dtype == yt and (pre is None) == (M == 40)
+        _check_forward(x, W, bias, residual, name, y, pre)
+        y2, _ = P.pkm_linear_forward(x, W, None, None, name, out_dtype=yt)
+        _check_forward(x, W, None, None, name, y2, None)
+
+
+def test_forward_residual_in_place_and_repeatable():
+    import product_key_memory_b200 as P
+    for M in (6, 700):
+        x, W, rn = _data(M, 264, 512, BF16)
+        residual = rn(M, 264).to(BF16)
+        want, _ = P.pkm_linear_forward(x, W, None, residual, "gelu")
+        again, _ = P.pkm_linear_forward(x, W, None, residual, "gelu")
+        buf = residual.clone()
+        got, _ = P.pkm_linear_forward(x, W, None, buf, "gelu", out=buf)
+        assert got.data_ptr() == buf.data_ptr()
+        assert torch.equal(got, want) and torch.equal(again, want)
+
+
+@pytest.mark.parametrize("kind", [BF16, F32])
+def test_a_non_finite_row_stays_its_own(kind):
+    """Rows of a tile share MMAs; a row of x with a NaN or an infinity does not reach the others,
+    nor does what lies behind the last row or column."""
+    import product_key_memory_b200 as P
+    for M, N, K in ((5, 40, 72), (150, 70, 100), (2100, 2056, 72)):
+        x, W, rn = _data(M, N, K, kind, seed=1)
+        want, _ = P.pkm_linear_forward(x, W, activation="silu")
+        for value in (float("nan"), float("inf")):
+            bad = x.clone()
+            bad[3, K // 2] = value
+            got, _ = P.pkm_linear_forward(bad, W, activation="silu")
+            keep = torch.arange(M, device="cuda") != 3
+            assert torch.equal(got[keep], want[keep])
+            plain = act(bad[3:4].double() @ W.double().t(), "silu")
+            assert not bool(got[3][~plain[0].isfinite()].isfinite().logical_and(
+                plain[0][~plain[0].isfinite()].isnan()).any())
+
+
+def _check_backward(x, W, gy, pre, name, grads):
+    f32 = x.dtype == F32
+    M, K = x.shape
+    N = W.shape[0]
+    xd, wd, gd = x.double(), W.double(), gy.double()
+    slope = act_slope(pre.double(), name) if name != "none" else torch.ones_like(gd)
+    d = gd * slope
+    # d itself: the slope's 8 roundings (of 1.13, and of its argument) and the product's
+    dd = gd.abs() * 10 * U * 1.13 if name in ("gelu", "silu") else U * d.abs()
+    pairs = 6 if f32 else (2 if name != "none" else 1)
+    cut = 2.0 ** -22 if f32 else (2.0 ** -17 if name != "none" else 0.0)
+    if "x" in grads:
+        gx = grads["x"]
+        one = not f32 and name != "none" and gx.dtype == BF16      # d rounded to bf16
+        c = half_step(BF16) if one else cut
+        b = _product_bound(d.abs() @ wd.abs(), N, 1 if one else pairs, c) + dd @ wd.abs()
+        r = d @ wd
+        assert_within("grad_x", gx, r, b + half_step(gx.dtype) * (r.abs() + b))
+    if "W" in grads:
+        b = _product_bound(d.abs().t() @ xd.abs(), M, pairs, cut) + dd.t() @ xd.abs()
+        assert_within("grad_W", grads["W"], d.t() @ xd, b)
+    if "bias" in grads:
+        b = (M + 16) * U * d.abs().sum(0) + dd.sum(0)
+        assert_within("grad_bias", grads["bias"], d.sum(0), b)
+
+
+BACK = [(1, 1, 1), (1, 64, 72), (2, 33, 65), (7, 515, 1001), (16, 130, 72), (64, 4096, 1024),
+        (129, 257, 8), (300, 1600, 264), (777, 515, 1001), (3000, 72, 80), (520, 2048, 1536),
+        (2100, 2056, 1000), (2049, 2305, 77)]
+
+
+@pytest.mark.parametrize("M,N,K", BACK)
+@pytest.mark.parametrize("kind", [BF16, F32])
+def test_backward_sizes(M, N, K, kind):
+    import product_key_memory_b200 as P
+    x, W, rn = _data(M, N, K, kind)
+    i = M + N + K + (kind == F32)
+    name = ACTS[i % 4]
+    gx, check_x = guarded((M, K), F32 if i % 3 == 0 else kind)
+    gW, check_W = guarded((N, K), F32)
+    gb, check_b = guarded((N,), F32)
+    pre = rn(M, N).to(kind) if name != "none" else None
+    gy = rn(M, N).to(kind)
+    shape = P.make_linear_shape(M, N, K, kind, gx.dtype, name)
+    ws = P.alloc_linear_workspace(shape, True, "cuda").fill_(255)
+    grads = dict(x=gx, W=gW, bias=gb)
+    P.pkm_linear_backward(x, W, gy, grads, pre=pre, activation=name, workspace=ws)
+    assert P.pkm_device_status(ws) == 0
+    _check_backward(x, W, gy, pre, name, grads)
+    check_x()
+    check_W()
+    check_b()
+
+
+@pytest.mark.parametrize("kind", [BF16, F32])
+@pytest.mark.parametrize("xt", [BF16, F32])
+@pytest.mark.parametrize("name", ACTS)
+def test_backward_types_and_subsets(kind, xt, name):
+    import product_key_memory_b200 as P
+    M, N, K = 210, 136, 88
+    x, W, rn = _data(M, N, K, kind, seed=2)
+    pre = rn(M, N).to(kind)
+    gy = rn(M, N).to(kind)
+    full = dict(x=torch.empty(M, K, device="cuda", dtype=xt), W=torch.empty(N, K, device="cuda"),
+                bias=torch.empty(N, device="cuda"))
+    P.pkm_linear_backward(x, W, gy, full, pre=pre, activation=name)
+    _check_backward(x, W, gy, pre, name, full)
+    for keys in (("x",), ("W",), ("bias",), ("W", "bias")):
+        some = {k: torch.full_like(full[k], 9.0) for k in keys}
+        P.pkm_linear_backward(x, W, gy, some, pre=pre, activation=name)
+        for k in keys:
+            # the same products whatever else is asked for; without x, out_dtype plays no part
+            assert torch.equal(some[k], full[k]), k
+
+
+def test_backward_against_differences():
+    """Central differences of sum(y gy) in 64 bits against the kernel's gradients along random
+    directions, gelu."""
+    import product_key_memory_b200 as P
+    M, N, K = 50, 70, 90
+    x, W, rn = _data(M, N, K, F32, seed=3)
+    bias, gy = rn(N), rn(M, N)
+    _, pre = P.pkm_linear_forward(x, W, bias, activation="gelu", want_pre=True)
+    grads = dict(x=torch.empty_like(x), W=torch.empty_like(W), bias=torch.empty_like(bias))
+    P.pkm_linear_backward(x, W, gy, grads, pre=pre, activation="gelu")
+    dirs = dict(x=rn(M, K).double(), W=rn(N, K).double() * K ** -0.5, bias=rn(N).double())
+
+    def loss(e):
+        p = (x.double() + e * dirs["x"]) @ (W.double() + e * dirs["W"]).t()
+        return (act(p + bias.double() + e * dirs["bias"], "gelu") * gy.double()).sum()
+
+    e = 1e-5
+    want = (loss(e) - loss(-e)) / (2 * e)
+    got = sum((grads[k].double() * dirs[k]).sum() for k in dirs)
+    size = sum((grads[k].double() * dirs[k]).abs().sum() for k in dirs)
+    # products of 90 terms: 2^-23 (6 * 90 / 16 + 16) + 2^-22 of terms a few times their sum;
+    # the difference's third-order term e^2
+    assert abs(got - want) <= 1e-4 * size
+
+
+def test_no_rows():
+    import product_key_memory_b200 as P
+    x, W = torch.empty(0, 40, device="cuda"), torch.ones(24, 40, device="cuda")
+    y, pre = P.pkm_linear_forward(x, W, want_pre=True)
+    assert y.shape == (0, 24) and pre.shape == (0, 24)
+    g = dict(x=torch.empty(0, 40, device="cuda"), W=torch.ones(24, 40, device="cuda"),
+             bias=torch.ones(24, device="cuda"))
+    P.pkm_linear_backward(x, W, y, g)
+    assert not bool(g["W"].any()) and not bool(g["bias"].any())
+
+
+def test_another_stream_two_at_once_and_captured_graph():
+    import product_key_memory_b200 as P
+    cases = []
+    for M in (4, 600, 2100):
+        x, W, rn = _data(M, 2056, 512, BF16)
+        gy = rn(M, 2056).to(BF16)
+        cases.append((x, W, rn(2056), gy))
+
+    def both(x, W, bias, gy, stream=None, spaces=(None, None)):
+        y, pre = P.pkm_linear_forward(x, W, bias, activation="gelu", want_pre=True, stream=stream,
+                                      workspace=spaces[0])
+        g = dict(x=torch.empty_like(x), W=torch.empty(W.shape, device="cuda"),
+                 bias=torch.empty_like(bias))
+        P.pkm_linear_backward(x, W, gy, g, pre=pre, activation="gelu", stream=stream,
+                              workspace=spaces[1])
+        return [y, pre, g["x"], g["W"], g["bias"]]
+    want = [both(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [both(*c, stream=s) for c, s in zip(cases, streams)]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+    for c, w in zip(cases, want):
+        fixed = [t.clone() for t in c]
+        side = streams[0]
+        with torch.cuda.stream(side):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                out = both(*fixed)
+        for t in fixed:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for t, s in zip(fixed, c):
+            t.copy_(s)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(out, w))
