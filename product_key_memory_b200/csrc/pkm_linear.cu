@@ -270,7 +270,8 @@ struct Plan {
   int ksplit;
 };
 
-Plan plan_gemm(int64_t M, int64_t N, int64_t steps) {
+Plan plan_gemm(int64_t M, int64_t N, int64_t K, int pairs) {
+  const int64_t blocks = (K + 63) / 64;
   const auto tiles = [&](int rows, int cols) {
     return ((M + rows - 1) / rows) * ((N + cols - 1) / cols);
   };
@@ -280,10 +281,11 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t steps) {
   const int64_t t = tiles(128, 64);
   int64_t split = sms / t;
   if (split > kMaxSplit) split = kMaxSplit;
-  if (split > steps / 4) split = steps / 4;   // at least four K steps each
+  if (split > blocks * pairs / 4) split = blocks * pairs / 4;   // at least four steps each
+  if (split > blocks) split = blocks;
   if (split <= 1) return {kTile64, 1};
-  const int64_t per = (steps + split - 1) / split;
-  return {kTile64, static_cast<int>((steps + per - 1) / per)};
+  const int64_t per = (blocks + split - 1) / split;             // no split is empty
+  return {kTile64, static_cast<int>((blocks + per - 1) / per)};
 }
 
 struct PlaneSet {
@@ -291,14 +293,12 @@ struct PlaneSet {
   int pairs;
 };
 
-// The plane pairs of a product: p + q below the larger plane count.
+// The plane pairs of a product, p + q below the larger plane count, smallest first.
 PlaneSet plane_pairs(int a, int b) {
-  if (a == 3 && b == 3) return {0x210100u, 0x012010u, 6};
-  if (a == 2) return {0x10u, 0x00u, 2};
+  if (a == 3 && b == 3) return {0x001012u, 0x010210u, 6};   // (2,0) (1,1) (0,2) (1,0) (0,1) (0,0)
+  if (a == 2) return {0x01u, 0x00u, 2};                     // (1,0) (0,0)
   return {0u, 0u, 1};
 }
-
-int64_t k_steps(int64_t K, int pairs) { return (K + 63) / 64 * pairs; }
 
 // Number of planes of an operand of the layer's type; in place (0 bytes) for bf16 rows of
 // 16-byte multiples.
@@ -337,15 +337,15 @@ Layout layout(const LinearArgs& a, bool backward) {
   l.part = off;
   if (!backward) {
     l.fwd_p = plane_pairs(in, in);
-    l.fwd = plan_gemm(a.M, a.N, k_steps(a.K, l.fwd_p.pairs));
+    l.fwd = plan_gemm(a.M, a.N, a.K, l.fwd_p.pairs);
     off += part_bytes(l.fwd, a.M, a.N);
   } else {
     const int d = slope_planes(a);
     // grad_x in bf16: d's rounding to bf16 is no larger than grad_x's own, one plane will do.
     l.gx_p = plane_pairs(d == 2 && a.out_dtype == PKM_BF16 ? 1 : (d ? d : 1), in);
     l.gw_p = plane_pairs(d ? d : 1, in);
-    l.gx = plan_gemm(a.M, a.K, k_steps(a.N, l.gx_p.pairs));
-    l.gw = plan_gemm(a.N, a.K, k_steps(a.M, l.gw_p.pairs));
+    l.gx = plan_gemm(a.M, a.K, a.N, l.gx_p.pairs);
+    l.gw = plan_gemm(a.N, a.K, a.M, l.gw_p.pairs);
     const size_t px = part_bytes(l.gx, a.M, a.K), pw = part_bytes(l.gw, a.N, a.K);
     off += px > pw ? px : pw;    // the two products run one after the other
     l.d = off;

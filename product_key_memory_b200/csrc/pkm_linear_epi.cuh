@@ -8,23 +8,43 @@
 
 namespace pkm {
 
-// gelu is v Phi(v) with Phi(v) = erfc(-v / sqrt 2) / 2 (no cancellation for negative v);
-// silu is v / (1 + exp(-v)). relu keeps a NaN.
+// erfc(x) / 2 and exp(-x^2) for x >= 0 by Abramowitz and Stegun 7.1.26: a polynomial of
+// t = 1 / (1 + p x) times exp(-x^2), within 0.75e-7 (a rounding of the 1 + erf(x) that it
+// stands for) and falling with exp(-x^2). A third of erfcf's instructions: the epilogue of
+// a product has about 32 per element before it takes longer than the product.
+__device__ __forceinline__ float half_erfc(float x, float* gauss) {
+  const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
+  float q = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
+  q = fmaf(q, t, 0.5f * 1.421413741f);
+  q = fmaf(q, t, 0.5f * -0.284496736f);
+  q = fmaf(q, t, 0.5f * 0.254829592f);
+  *gauss = __expf(-x * x);
+  return q * t * *gauss;
+}
+
+// gelu is v Phi(v) with Phi(v) = erfc(-v / sqrt 2) / 2, mirrored for v > 0; silu is
+// v / (1 + exp(-v)). relu keeps a NaN.
 __device__ __forceinline__ float act_value(float v, int act) {
   if (act == PKM_ACT_RELU) return v <= 0.f ? 0.f : v;
-  if (act == PKM_ACT_GELU) return 0.5f * v * erfcf(v * -0.70710678118654752f);
-  if (act == PKM_ACT_SILU) return v / (1.f + expf(-v));
+  if (act == PKM_ACT_GELU) {
+    float gauss;
+    const float q = half_erfc(fabsf(v) * 0.70710678118654752f, &gauss);
+    return v * (v > 0.f ? 1.f - q : q);
+  }
+  if (act == PKM_ACT_SILU) return __fdividef(v, 1.f + __expf(-v));
   return v;
 }
 
 // d act / d v. gelu' = Phi(v) + v phi(v), silu' = s (1 + v (1 - s)) with s = 1/(1 + exp(-v)).
 __device__ __forceinline__ float act_slope(float v, int act) {
   if (act == PKM_ACT_RELU) return v <= 0.f ? 0.f : (v > 0.f ? 1.f : v);
-  if (act == PKM_ACT_GELU)
-    return fmaf(v * 0.39894228040143268f, expf(-0.5f * v * v),
-                0.5f * erfcf(v * -0.70710678118654752f));
+  if (act == PKM_ACT_GELU) {
+    float gauss;
+    const float q = half_erfc(fabsf(v) * 0.70710678118654752f, &gauss);
+    return fmaf(v * 0.39894228040143268f, gauss, v > 0.f ? 1.f - q : q);
+  }
   if (act == PKM_ACT_SILU) {
-    const float s = 1.f / (1.f + expf(-v));
+    const float s = __fdividef(1.f, 1.f + __expf(-v));
     return s * fmaf(v, 1.f - s, 1.f);
   }
   return 1.f;
@@ -44,64 +64,6 @@ __device__ __forceinline__ void linear_store1(const LinearEpilogue& e, int64_t a
   } else {
     if (e.residual) v += __bfloat162float(static_cast<const __nv_bfloat16*>(e.residual)[at]);
     static_cast<__nv_bfloat16*>(e.y)[at] = __float2bfloat16_rn(v);
-  }
-}
-
-// Eight consecutive columns of one row; `at` and `col` are multiples of 8.
-__device__ __forceinline__ void linear_store8(const LinearEpilogue& e, int64_t at, int col,
-                                              float* v) {
-  if (e.bias) {
-    float b[8];
-    load_param<8>(e.bias, col, b);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += b[i];
-  }
-  if (e.pre) {
-    if (e.pre_f32) Out<F32, 8>::store(e.pre, at, v);
-    else Out<BF16, 8>::store(e.pre, at, v);
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = act_value(v[i], e.act);
-  if (e.residual) {
-    float r[8];
-    if (e.y_f32) {
-      Raw<F32, 8> q;
-      q.load(e.residual, at);
-      q.get(r);
-    } else {
-      Raw<BF16, 8> q;
-      q.load(e.residual, at);
-      q.get(r);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += r[i];
-  }
-  if (e.y_f32) Out<F32, 8>::store(e.y, at, v);
-  else Out<BF16, 8>::store(e.y, at, v);
-}
-
-// 32 consecutive columns from `col` (a multiple of 32) of one row; columns from N on do
-// not exist.
-__device__ __forceinline__ void linear_store_row32(const LinearEpilogue& e, int row, int col,
-                                                   int M, int N, int split, float* v) {
-  if (e.part) {
-    float* p = e.part + (static_cast<int64_t>(split) * M + row) * e.ldp + col;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)   // ldp covers the last group of four
-      if (col + 4 * i < N)
-        reinterpret_cast<float4*>(p)[i] =
-            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    return;
-  }
-  const int64_t at = static_cast<int64_t>(row) * N + col;
-  if ((N & 7) == 0) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (col + 8 * i < N) linear_store8(e, at + 8 * i, col + 8 * i, v + 8 * i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (col + i < N) linear_store1(e, at + i, col + i, v[i]);
   }
 }
 

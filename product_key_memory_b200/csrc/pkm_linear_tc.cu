@@ -17,6 +17,18 @@
 // a pair of CTAs shares each MMA (cta_group::2), every CTA loading half of A's rows and
 // half of B's columns. Every wait is bounded as in the query kernel; the pair leaves
 // through a cluster barrier, so neither CTA exits under the other's copies or MMAs.
+//
+// Accumulation: the tensor cores cut the running sum at each step of 16 products, about
+// 2^-24 of it towards zero, so K / 16 cuts add up (1e-5 of the result at K = 8192). Where
+// the output is fp32 (PROMOTE) the accumulator is therefore taken out every kSegment K
+// blocks and added to fp32 registers, rounded to nearest; the epilogue warps do that while
+// the next segment is multiplied into the other half of TMEM. Plane pairs go smallest
+// first inside a segment, so the small ones are added to small sums.
+//
+// Epilogue: a thread owns a row of 32 columns at a time. Rows go through shared memory,
+// swizzled, and leave as TMA stores of 32 x 32 (a thread's own 16-byte stores would touch
+// a line per lane); outputs whose rows are no multiple of 16 bytes go out a row at a
+// time, lanes along the columns.
 #include "pkm_linear_epi.cuh"
 #include "pkm_tc.h"
 #include "pkm_tcgen05.cuh"
@@ -31,15 +43,19 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kRows = 128;               // rows of a tile per CTA
 constexpr int kK = 64;                   // K per stage: one 128-byte swizzled row of bf16
+constexpr int kSegment = 4;              // K blocks between two takings (PROMOTE)
 constexpr uint32_t kABytes = kRows * kK * 2;
 constexpr uint32_t kMnBlock = 64 * kK * 2;   // 64 MN x 64 K of an MN-major operand
+// Staging of one epilogue warp: 32 x 32 outputs of y and pre, 4 KiB of either in fp32, 2 in
+// bf16; two sets of buffers in turn where both fit twice.
+constexpr uint32_t kStaging = 8192;
 
 template <int CG, int BN> struct Tile {
   static constexpr int kCols = BN / CG;                      // of B per CTA
   static constexpr uint32_t kBBytes = kCols * kK * 2;
   static constexpr uint32_t kStage = kABytes + kBBytes;
-  static constexpr int kStages = 196608 / kStage;            // 192 KiB of stages
-  static constexpr size_t kSmem = 1024 + kStages * kStage + 512;
+  static constexpr int kStages = 163840 / kStage;            // 160 KiB of stages
+  static constexpr size_t kSmem = 1024 + kStages * kStage + kEpiWarps * kStaging + 512;
   static constexpr uint32_t kTmemCols = 2 * BN;
 };
 
@@ -54,15 +70,182 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t addr) {
          ((1024ull >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-template <bool A_MN, bool B_MN, int CG, int BN>
+// Step i of a product runs over segments of `seg` K blocks, in each over the plane pairs,
+// in each over the K blocks.
+struct Step {
+  int kb, pair;
+};
+__device__ __forceinline__ Step step_at(int i, int kblocks, int seg, int pairs) {
+  const int s = i / (seg * pairs), r = i - s * (seg * pairs);
+  const int here = min(seg, kblocks - s * seg);
+  const int pr = r / here;
+  return {s * seg + r - pr * here, pr};
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                       uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+
+__device__ __forceinline__ float4 lds128(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// Shared-memory address of the 16-byte chunk c of row r of a 32 x 32 tile: 128-byte rows
+// (fp32) or 64-byte rows (bf16) with the matching TMA swizzle.
+__device__ __forceinline__ uint32_t tile_chunk(uint32_t base, int r, int c, bool f32) {
+  return f32 ? base + r * 128 + ((c ^ (r & 7)) << 4) : base + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+__device__ __forceinline__ void stage_row(uint32_t base, int r, bool f32, const float* v) {
+  if (f32) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      sts128(tile_chunk(base, r, c, true), __float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
+             __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      sts128(tile_chunk(base, r, c, false), pack_bf16(v[8 * c], v[8 * c + 1]),
+             pack_bf16(v[8 * c + 2], v[8 * c + 3]), pack_bf16(v[8 * c + 4], v[8 * c + 5]),
+             pack_bf16(v[8 * c + 6], v[8 * c + 7]));
+  }
+}
+
+// A warp's 32 x 32 block of the residual into its staging area (whole 16-byte chunks: the
+// rows are multiples of 16 bytes), lanes along the rows' chunks.
+__device__ __forceinline__ void stage_residual(uint32_t base, const void* residual, bool f32,
+                                               int row0, int col, int M, int N, int lane) {
+  const int per = f32 ? 8 : 4;              // chunks a row
+  const int wide = f32 ? 4 : 8;             // columns a chunk
+  const int c = lane & (per - 1);
+  for (int r = lane / per; r < 32; r += 32 / per) {
+    uint4 q = make_uint4(0, 0, 0, 0);
+    if (row0 + r < M && col + c * wide < N) {
+      const int64_t at = static_cast<int64_t>(row0 + r) * N + col + c * wide;
+      q = *reinterpret_cast<const uint4*>(static_cast<const char*>(residual) +
+                                          at * (f32 ? 4 : 2));
+    }
+    sts128(tile_chunk(base, r, c, f32), q.x, q.y, q.z, q.w);
+  }
+}
+
+__device__ __forceinline__ void add_residual(uint32_t base, int r, bool f32, float* v) {
+  if (f32) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float4 q = lds128(tile_chunk(base, r, c, true));
+      v[4 * c] += q.x; v[4 * c + 1] += q.y; v[4 * c + 2] += q.z; v[4 * c + 3] += q.w;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float4 q = lds128(tile_chunk(base, r, c, false));
+      const uint32_t w[4] = {__float_as_uint(q.x), __float_as_uint(q.y), __float_as_uint(q.z),
+                             __float_as_uint(q.w)};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[8 * c + 2 * k] += bf16_lo(w[k]);
+        v[8 * c + 2 * k + 1] += bf16_hi(w[k]);
+      }
+    }
+  }
+}
+
+// The epilogue of one warp: its staging area and what it knows of the outputs' layout.
+struct Outputs {
+  uint32_t staging;      // shared address, 1024-byte aligned
+  uint32_t pre_at, set;  // offset of pre's block, bytes of one set of buffers
+  int sets, turn;
+  bool tma;              // rows are multiples of 16 bytes
+};
+
+// 32 rows x 32 columns of the result: this thread's row `row0 + lane` in v, columns from
+// `col`. Warp-uniform arguments but v.
+__device__ __forceinline__ void store_block(const CUtensorMap* tm_y, const CUtensorMap* tm_pre,
+                                            const LinearEpilogue& e, Outputs& o, int row0, int col,
+                                            int M, int N, int split, int lane, float* v) {
+  const bool part = e.part != nullptr;
+  const bool yf = part || e.y_f32;
+  if (o.tma) {
+    const uint32_t y = o.staging + o.turn * o.set, p = y + o.pre_at;
+    // The set's previous stores have read it: all but the last group, or all of them.
+    if (lane == 0) {
+      if (o.sets == 2) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      else bulk_wait_read0();
+    }
+    __syncwarp();
+    if (!part) {
+      if (e.residual) stage_residual(y, e.residual, e.y_f32, row0, col, M, N, lane);
+      if (e.bias) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          if (col + i < N) {   // N is a multiple of 4
+            const float4 b = __ldg(reinterpret_cast<const float4*>(e.bias + col + i));
+            v[i] += b.x; v[i + 1] += b.y; v[i + 2] += b.z; v[i + 3] += b.w;
+          }
+        }
+      }
+      if (e.pre) stage_row(p, lane, e.pre_f32, v);
+      if (e.act == PKM_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], PKM_ACT_RELU);
+      } else if (e.act == PKM_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], PKM_ACT_GELU);
+      } else if (e.act == PKM_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], PKM_ACT_SILU);
+      }
+      if (e.residual) {
+        __syncwarp();   // the other lanes' chunks of this row
+        add_residual(y, lane, e.y_f32, v);
+      }
+    }
+    stage_row(y, lane, yf, v);   // the row that this thread alone has read
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_3d_at(tm_y, y, col, row0, part ? split : 0);
+      if (e.pre && !part) tma_store_3d_at(tm_pre, p, col, row0, 0);
+      bulk_commit();
+    }
+    if (o.sets == 2) o.turn ^= 1;
+    return;
+  }
+  // Rows of any length: transposed through shared memory, 33 words a row, then a row at a
+  // time with the lanes along the columns.
+  const uint32_t base = o.staging;
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) sts_f32(base + (lane * 33 + i) * 4, v[i]);
+  __syncwarp();
+  if (col + lane < N) {
+    const int rows = min(32, M - row0);
+    for (int r = 0; r < rows; ++r)
+      linear_store1(e, static_cast<int64_t>(row0 + r) * N + col + lane, col + lane,
+                    lds_f32(base + (r * 33 + lane) * 4));
+  }
+}
+
+template <bool A_MN, bool B_MN, int CG, int BN, bool PROMOTE>
 __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(
-    const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, int M,
-    int N, int K, uint32_t a_planes, uint32_t b_planes, int pairs, int ksplit,
+    const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+    const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_pre, int M,
+    int N, int K, uint32_t a_planes, uint32_t b_planes, int pairs, int ksplit, int use_tma,
     const LinearEpilogue epi, int* status) {
   using T = Tile<CG, BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = align1024(smem_raw);
-  uint64_t* full = reinterpret_cast<uint64_t*>(stages + T::kStages * T::kStage);
+  uint8_t* staging = stages + T::kStages * T::kStage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStaging);
   uint64_t* empty = full + T::kStages;
   uint64_t* tfull = empty + T::kStages;
   uint64_t* tempty = tfull + 2;
@@ -75,8 +258,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(
   const int mt = (M + CG * kRows - 1) / (CG * kRows);
   const int nt = (N + BN - 1) / BN;
   const int ntiles = mt * nt * ksplit;
-  const int steps = (K + kK - 1) / kK * pairs;      // K blocks x plane pairs
-  const int per = (steps + ksplit - 1) / ksplit;
+  // A split takes `per` K blocks, a segment `seg` of those.
+  const int all = (K + kK - 1) / kK;
+  const int per = (all + ksplit - 1) / ksplit;
+  const int seg = PROMOTE ? kSegment : per;
   const int first = blockIdx.x / CG, stride = gridDim.x / CG;
 
   if (threadIdx.x == 0) {
@@ -114,14 +299,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(
         const int sp = t % ksplit, mn = t / ksplit;
         const int m0 = (mn / nt) * (CG * kRows) + rank * kRows;
         const int n0 = (mn % nt) * BN + rank * T::kCols;
-        const int i0 = sp * per, i1 = min(steps, i0 + per);
-        for (int i = i0; i < i1; ++i) {
+        const int kblocks = min(per, all - sp * per);
+        for (int i = 0; i < kblocks * pairs; ++i) {
           if (!mbar_wait(&empty[s], ph ^ 1, status, abort)) { ok = false; break; }
           uint8_t* a = stages + s * T::kStage;
           uint8_t* b = a + kABytes;
-          const int kb = i / pairs, pr = i - kb * pairs;
-          const int k0 = kb * kK;
-          const int pa = (a_planes >> (4 * pr)) & 15, pb = (b_planes >> (4 * pr)) & 15;
+          const Step at = step_at(i, kblocks, seg, pairs);
+          const int k0 = (sp * per + at.kb) * kK;
+          const int pa = (a_planes >> (4 * at.pair)) & 15, pb = (b_planes >> (4 * at.pair)) & 15;
           uint32_t bar;
           if (CG == 2) {
             bar = leader_addr(&full[s]);
@@ -170,30 +355,33 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(
       uint32_t s = 0, ph = 0;
       bool ok = true;
       int it = 0;
-      for (int t = first; t < ntiles && ok; t += stride, ++it) {
+      for (int t = first; t < ntiles && ok; t += stride) {
         const int sp = t % ksplit;
-        const int i0 = sp * per, i1 = min(steps, i0 + per);
-        const int buf = it & 1;
-        const uint32_t tph = (it >> 1) & 1;
-        if (!mbar_wait(&tempty[buf], tph ^ 1, status, abort)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + buf * BN;
-        for (int i = i0; i < i1; ++i) {
-          if (!mbar_wait(&full[s], ph, status, abort)) { ok = false; break; }
+        const int kblocks = min(per, all - sp * per);
+        for (int k = 0; k < kblocks && ok; k += seg, ++it) {
+          const int here = min(seg, kblocks - k) * pairs;
+          const int buf = it & 1;
+          const uint32_t tph = (it >> 1) & 1;
+          if (!mbar_wait(&tempty[buf], tph ^ 1, status, abort)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t a = smem_addr(stages + s * T::kStage);
-          const uint32_t b = a + kABytes;
+          const uint32_t d_tmem = tmem_base + buf * BN;
+          for (int i = 0; i < here; ++i) {
+            if (!mbar_wait(&full[s], ph, status, abort)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t a = smem_addr(stages + s * T::kStage);
+            const uint32_t b = a + kABytes;
 #pragma unroll
-          for (int j = 0; j < kK / 16; ++j) {
-            // 16 K = two 8-row atoms of an MN-major tile, 32 bytes of a K-major row.
-            const uint64_t ad = A_MN ? mn_desc(a + j * 2048) : sw128_desc(a, j * 32);
-            const uint64_t bd = B_MN ? mn_desc(b + j * 2048) : sw128_desc(b, j * 32);
-            mma_bf16_cg<CG>(d_tmem, ad, bd, idesc, (i != i0 || j != 0) ? 1u : 0u);
+            for (int j = 0; j < kK / 16; ++j) {
+              // 16 K = two 8-row atoms of an MN-major tile, 32 bytes of a K-major row.
+              const uint64_t ad = A_MN ? mn_desc(a + j * 2048) : sw128_desc(a, j * 32);
+              const uint64_t bd = B_MN ? mn_desc(b + j * 2048) : sw128_desc(b, j * 32);
+              mma_bf16_cg<CG>(d_tmem, ad, bd, idesc, (i != 0 || j != 0) ? 1u : 0u);
+            }
+            mma_commit_all<CG>(&empty[s]);
+            if (++s == T::kStages) { s = 0; ph ^= 1; }
           }
-          mma_commit_all<CG>(&empty[s]);
-          if (++s == T::kStages) { s = 0; ph ^= 1; }
+          if (ok) mma_commit_all<CG>(&tfull[buf]);
         }
-        if (ok) mma_commit_all<CG>(&tfull[buf]);
       }
       mma_commit_all<CG>(drain);
       const uint64_t t0 = global_timer_ns();
@@ -206,33 +394,77 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(
     const int quad = warp & 3;
     const int cset = (warp - 2) >> 2;
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
+    const bool part = epi.part != nullptr;
+    Outputs o;
+    o.staging = smem_addr(staging + (warp - 2) * kStaging);
+    o.pre_at = part || epi.y_f32 ? 4096 : 2048;
+    o.set = o.pre_at + (epi.pre && !part ? (epi.pre_f32 ? 4096 : 2048) : 0);
+    o.sets = o.set * 2 <= kStaging ? 2 : 1;
+    o.turn = 0;
+    o.tma = use_tma;
     int it = 0;
-    for (int t = first; t < ntiles; t += stride, ++it) {
-      const int buf = it & 1;
-      const uint32_t tph = (it >> 1) & 1;
-      if (!warp_wait(&tfull[buf], tph, status, abort)) break;
-      tc_fence_after();
+    bool ok = true;
+    for (int t = first; t < ntiles && ok; t += stride) {
       const int sp = t % ksplit, mn = t / ksplit;
-      const int row = (mn / nt) * (CG * kRows) + rank * kRows + quad * 32 + lane;
-      const int n0 = (mn % nt) * BN;
-#pragma unroll 1
-      for (int gg = 0; gg < kGroups; ++gg) {
-        const int g = cset * kGroups + gg;
-        float v[32];
-        __syncwarp();
-        tmem_ld32(tmem_base + lane_addr + buf * BN + g * 32, v);
-        if (gg == kGroups - 1) {
+      const int row0 = (mn / nt) * (CG * kRows) + rank * kRows + quad * 32;
+      const int n0 = (mn % nt) * BN + cset * (BN / 2);
+      const int segments = (min(per, all - sp * per) + seg - 1) / seg;
+      float acc[PROMOTE ? kGroups : 1][32];
+      if (PROMOTE) {
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[PROMOTE ? g : 0][i] = 0.f;
+      }
+      for (int k = 0; k < segments; ++k, ++it) {
+        const int buf = it & 1;
+        const uint32_t tph = (it >> 1) & 1;
+        if (!warp_wait(&tfull[buf], tph, status, abort)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + lane_addr + buf * BN + cset * (BN / 2);
+        if (PROMOTE) {
+#pragma unroll
+          for (int h = 0; h < 2 * kGroups; ++h) {
+            float v[16];
+            __syncwarp();
+            tmem_ld16(d_tmem + h * 16, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[PROMOTE ? h / 2 : 0][(h & 1) * 16 + i] += v[i];
+          }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
             if (CG == 2) mbar_arrive_cluster(leader_addr(&tempty[buf]));
             else mbar_arrive(&tempty[buf]);
           }
+        } else {
+#pragma unroll 1
+          for (int g = 0; g < kGroups; ++g) {
+            float v[32];
+            __syncwarp();
+            tmem_ld32(d_tmem + g * 32, v);
+            if (g == kGroups - 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                if (CG == 2) mbar_arrive_cluster(leader_addr(&tempty[buf]));
+                else mbar_arrive(&tempty[buf]);
+              }
+            }
+            if (row0 < M && n0 + g * 32 < N)
+              store_block(&tm_y, &tm_pre, epi, o, row0, n0 + g * 32, M, N, sp, lane, v);
+          }
         }
-        const int col = n0 + g * 32;
-        if (row < M && col < N) linear_store_row32(epi, row, col, M, N, sp, v);
+      }
+      if (PROMOTE && ok) {
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+          if (row0 < M && n0 + g * 32 < N)
+            store_block(&tm_y, &tm_pre, epi, o, row0, n0 + g * 32, M, N, sp, lane,
+                        acc[PROMOTE ? g : 0]);
       }
     }
+    if (lane == 0) bulk_wait0();   // the stores have left shared memory and landed
   }
   __syncwarp();
   tc_fence_before();
@@ -244,7 +476,19 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(
   }
 }
 
-template <bool A_MN, bool B_MN, int CG, int BN>
+// [planes][rows][cols] of an output, or of the parts of a split one.
+bool output_map(CUtensorMap* m, const void* p, bool f32, int64_t cols, int64_t ld, int64_t rows,
+                int planes) {
+  const cuuint64_t e = f32 ? 4 : 2;
+  const cuuint64_t d[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                           static_cast<cuuint64_t>(planes)};
+  const cuuint64_t s[2] = {static_cast<cuuint64_t>(ld) * e, static_cast<cuuint64_t>(ld * rows) * e};
+  const cuuint32_t b[3] = {32, 32, 1};
+  return make_map(m, p, 3, d, s, b, f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+}
+
+template <bool A_MN, bool B_MN, int CG, int BN, bool PROMOTE>
 cudaError_t run(const LinearGemm& g, cudaStream_t st) {
   using T = Tile<CG, BN>;
   CUtensorMap tm_a, tm_b;
@@ -259,9 +503,20 @@ cudaError_t run(const LinearGemm& g, cudaStream_t st) {
   const cuuint32_t bb[3] = {64, static_cast<cuuint32_t>(B_MN ? kK : T::kCols), 1};
   if (!make_map(&tm_a, g.a, 3, ad, as, ab) || !make_map(&tm_b, g.b, 3, bd, bs, bb))
     return cudaErrorInvalidValue;
-  auto* kernel = linear_tc_kernel<A_MN, B_MN, CG, BN>;
-  cudaError_t e = set_max_smem(reinterpret_cast<const void*>(kernel), T::kSmem);
-  if (e != cudaSuccess) return e;
+  // TMA stores need rows of 16-byte multiples (parts have them).
+  const LinearEpilogue& e = g.epi;
+  const bool yf = e.part || e.y_f32;
+  const int tma = e.part || (g.N % (e.y_f32 ? 4 : 8) == 0 && (!e.pre || e.pre_f32 || g.N % 8 == 0));
+  CUtensorMap tm_y = tm_a, tm_pre = tm_a;
+  if (tma) {
+    const bool ok = e.part ? output_map(&tm_y, e.part, true, e.ldp, e.ldp, g.M, g.ksplit)
+                           : output_map(&tm_y, e.y, yf, g.N, g.N, g.M, 1);
+    if (!ok || (!e.part && e.pre && !output_map(&tm_pre, e.pre, e.pre_f32, g.N, g.N, g.M, 1)))
+      return cudaErrorInvalidValue;
+  }
+  auto* kernel = linear_tc_kernel<A_MN, B_MN, CG, BN, PROMOTE>;
+  cudaError_t rc = set_max_smem(reinterpret_cast<const void*>(kernel), T::kSmem);
+  if (rc != cudaSuccess) return rc;
   const int tiles = ((g.M + CG * kRows - 1) / (CG * kRows)) * ((g.N + BN - 1) / BN) * g.ksplit;
   const int most = sm_count() / CG;
   cudaLaunchConfig_t cfg = {};
@@ -276,16 +531,24 @@ cudaError_t run(const LinearGemm& g, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG == 2 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, tm_a, tm_b, g.M, g.N, g.K, g.a_planes, g.b_planes,
-                            g.pairs, g.ksplit, g.epi, g.status);
+  return cudaLaunchKernelEx(&cfg, kernel, tm_a, tm_b, tm_y, tm_pre, g.M, g.N, g.K, g.a_planes,
+                            g.b_planes, g.pairs, g.ksplit, tma, g.epi, g.status);
+}
+
+template <bool A_MN, bool B_MN, int CG, int BN>
+cudaError_t promoted(const LinearGemm& g, cudaStream_t st) {
+  // fp32 results of more than one segment; a bf16 result's own rounding hides the cuts.
+  const bool exact = g.epi.y_f32 || (g.epi.pre && g.epi.pre_f32);
+  return exact && g.K > kSegment * kK ? run<A_MN, B_MN, CG, BN, true>(g, st)
+                                      : run<A_MN, B_MN, CG, BN, false>(g, st);
 }
 
 template <bool A_MN, bool B_MN>
 cudaError_t pick(const LinearGemm& g, cudaStream_t st) {
   switch (g.tile) {
-    case kTile256: return run<A_MN, B_MN, 2, 256>(g, st);
-    case kTile128: return run<A_MN, B_MN, 1, 128>(g, st);
-    default: return run<A_MN, B_MN, 1, 64>(g, st);
+    case kTile256: return promoted<A_MN, B_MN, 2, 256>(g, st);
+    case kTile128: return promoted<A_MN, B_MN, 1, 128>(g, st);
+    default: return promoted<A_MN, B_MN, 1, 64>(g, st);
   }
 }
 

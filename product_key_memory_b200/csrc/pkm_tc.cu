@@ -745,14 +745,15 @@ EncodeTiledFn encode_fn() {
 
 }  // namespace
 
-// bf16 tensor map with a {64 x rows} box and the 128-byte swizzle. dims/strides are
-// innermost first; strides are in bytes for dims 1.. (dim 0 is contiguous).
+// dims/strides are innermost first; strides are in bytes for dims 1.. (dim 0 is
+// contiguous).
 bool make_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
-              const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swz) {
+              const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swz,
+              CUtensorMapDataType type) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides,
+  return fn(m, type, rank, const_cast<void*>(base), dims, strides,
             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

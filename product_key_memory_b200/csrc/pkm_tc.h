@@ -27,10 +27,12 @@ cudaError_t launch_score_topk_tc(const LayerArgs& a, const void* planes, float* 
 // Streaming multiprocessors of the current device (cached).
 int sm_count();
 
-// bf16 tensor map; dims/strides innermost first, strides in bytes for dims 1..
+// Tensor map (bf16 unless said otherwise); dims/strides innermost first, strides in bytes
+// for dims 1..
 bool make_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
               const cuuint64_t* strides, const cuuint32_t* box,
-              CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B);
+              CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B,
+              CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 
 // Tensor-core GEMMs of the backward (pkm_gemm_tc.cu). g_planes holds dL/dacc as two
 // bf16 planes hi/lo [2][B][F]. grad_x [B][d] = dL/dacc W_q; grad_W [F][d] = dL/dacc^T x.
