@@ -10,6 +10,7 @@ importing this package raises if libpkm.so is missing. There is no CPU path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -429,58 +430,78 @@ def _dtype(t) -> int:
 
 def _check(name: str, t: torch.Tensor, shape, dtype, device) -> None:
     """t is a contiguous device tensor of this shape, type (None: fp32 or bf16) and device."""
+    kind = t.dtype
+    if (t.shape == shape and (kind is dtype or (dtype is None and kind in _DTYPES)) and
+            t.device == device and t.is_cuda and t.is_contiguous()):
+        return
     if tuple(t.shape) != tuple(shape):
         raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if dtype is None:
-        _dtype(t.dtype)
-    elif t.dtype != dtype:
-        raise ValueError("%s: %s, expected %s" % (name, t.dtype, dtype))
+        _dtype(kind)
+    elif kind != dtype:
+        raise ValueError("%s: %s, expected %s" % (name, kind, dtype))
     if not t.is_cuda:
         raise ValueError("%s: libpkm takes device tensors" % name)
     if t.device != device:
         raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
-    if not t.is_contiguous():
-        raise ValueError("%s: libpkm takes contiguous tensors" % name)
+    raise ValueError("%s: libpkm takes contiguous tensors" % name)
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 class _Call:
     """The device and stream of one call: makes `device` current while it lasts, and keeps
     what the call allocates from being reused before `stream` is done with it."""
+    __slots__ = ("device", "given", "handle", "guard")
 
     def __init__(self, device: torch.device, stream):
-        self.guard = torch.cuda.device(device)
-        self.device = device
-        self.given = stream
+        if stream is not None and stream.device != device:
+            raise ValueError("stream is on %s, not on %s" % (stream.device, device))
+        self.device, self.given, self.guard = device, stream, None
 
     def __enter__(self):
-        self.guard.__enter__()
-        current = torch.cuda.current_stream(self.device)
-        self.stream = current if self.given is None else self.given
-        self.other = self.stream != current
+        index = self.device.index
+        if _current_device() != index:
+            self.guard = torch.cuda.device(index)
+            self.guard.__enter__()
+        self.handle = _raw_stream(index)
+        if self.given is not None:
+            if self.given.cuda_stream == self.handle:
+                self.given = None
+            else:
+                self.handle = self.given.cuda_stream
         return self
 
     def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
     def empty(self, shape, dtype) -> torch.Tensor:
         t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.other:
-            t.record_stream(self.stream)
+        if self.given is not None:
+            t.record_stream(self.given)
         return t
-
-    @property
-    def handle(self):
-        return ctypes.c_void_p(self.stream.cuda_stream)
 
 
 def _addr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def make_norm_shape(rows, d, x_dtype=PKM_F32, add_dtype=PKM_F32, y_dtype=PKM_F32,
                     grad_dtype=PKM_F32, eps=1e-5) -> pkm_norm_shape:
     return pkm_norm_shape(int(rows), int(d), _dtype(x_dtype), _dtype(add_dtype), _dtype(y_dtype),
                           _dtype(grad_dtype), float(eps))
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_ref(*fields):
+    """(make_norm_shape(*fields) by reference, workspace bytes): sizes and types only."""
+    shape = make_norm_shape(*fields)
+    ref = ctypes.byref(shape)
+    return ref, int(lib().pkm_norm_workspace_size(ref))
 
 
 def alloc_norm_workspace(shape: pkm_norm_shape, device=None) -> torch.Tensor:
@@ -521,8 +542,8 @@ def pkm_layernorm_forward(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[t
     if sum_out is not None:
         _check("sum_out", sum_out, (rows, d), x.dtype, dev)
     out_dtype = out_dtype or x.dtype
-    shape = make_norm_shape(rows, d, x.dtype, PKM_F32 if add is None else add.dtype, out_dtype,
-                            PKM_F32, eps)
+    ref, _ = _norm_ref(rows, d, x.dtype, PKM_F32 if add is None else add.dtype, out_dtype, PKM_F32,
+                       eps)
     with _Call(dev, stream) as c:
         if out is None:
             out = c.empty((rows, d), out_dtype)
@@ -530,7 +551,7 @@ def pkm_layernorm_forward(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[t
             sum_out = c.empty((rows, d), x.dtype)
         mean = c.empty(rows, torch.float32) if want_stats else None
         rstd = c.empty(rows, torch.float32) if want_stats else None
-        rc = lib().pkm_layernorm_forward(ctypes.byref(shape), _addr(x), _addr(add), _addr(gamma),
+        rc = lib().pkm_layernorm_forward(ref, _addr(x), _addr(add), _addr(gamma),
                                          _addr(beta), _addr(out), _addr(sum_out), _addr(mean),
                                          _addr(rstd), c.handle)
     if rc != PKM_OK:
@@ -570,8 +591,8 @@ def pkm_layernorm_backward(grad_y: torch.Tensor, x: torch.Tensor, mean: torch.Te
     for name, t in (("grad_gamma", grad_gamma), ("grad_beta", grad_beta)):
         if t is not None:
             _check(name, t, (d,), torch.float32, dev)
-    shape = make_norm_shape(rows, d, x.dtype, PKM_F32 if grad_sum is None else grad_sum.dtype,
-                            grad_y.dtype, grad_dtype)
+    ref, need = _norm_ref(rows, d, x.dtype, PKM_F32 if grad_sum is None else grad_sum.dtype,
+                          grad_y.dtype, grad_dtype)
     with _Call(dev, stream) as c:
         if grad_x is None:
             grad_x = c.empty((rows, d), grad_dtype)
@@ -580,10 +601,9 @@ def pkm_layernorm_backward(grad_y: torch.Tensor, x: torch.Tensor, mean: torch.Te
         if grad_beta is None:
             grad_beta = c.empty(d, torch.float32)
         if workspace is None:
-            n = int(lib().pkm_norm_workspace_size(ctypes.byref(shape)))
-            workspace = c.empty(max(n, 1), torch.uint8)
+            workspace = c.empty(max(need, 1), torch.uint8)
         ws, nbytes = _given_workspace(c, workspace)
-        rc = lib().pkm_layernorm_backward(ctypes.byref(shape), _addr(grad_y), _addr(x),
+        rc = lib().pkm_layernorm_backward(ref, _addr(grad_y), _addr(x),
                                           _addr(mean), _addr(rstd), _addr(gamma), _addr(grad_sum),
                                           _addr(grad_x), _addr(grad_gamma), _addr(grad_beta),
                                           _addr(ws), nbytes, c.handle)
@@ -681,9 +701,12 @@ def pkm_adamw_step(tensors: AdamWTensors, lr: float, step: int, betas=(0.9, 0.99
         _check("dyn", dyn, (3,), torch.float32, tensors.device)
     h = pkm_adamw_hyper(float(lr), float(betas[0]), float(betas[1]), float(eps),
                         float(grad_scale), int(step), int(seed) & 0xffffffff, int(bool(zero_grad)))
-    with _Call(tensors.device, stream) as c:
-        rc = lib().pkm_adamw_step(tensors.array, len(tensors), ctypes.byref(h), _addr(dyn),
-                                  c.handle)
+    if len(tensors):
+        with _Call(tensors.device, stream) as c:
+            rc = lib().pkm_adamw_step(tensors.array, len(tensors), ctypes.byref(h), _addr(dyn),
+                                      c.handle)
+    else:
+        rc = lib().pkm_adamw_step(None, 0, ctypes.byref(h), None, None)
     if rc != PKM_OK:
         raise PKMError("pkm_adamw_step", rc)
 
@@ -718,11 +741,18 @@ def _given_workspace(c: _Call, workspace: torch.Tensor):
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def _linear_workspace(c: _Call, shape: pkm_linear_shape, workspace, for_backward: int):
+@functools.lru_cache(maxsize=1024)
+def _linear_ref(for_backward, *fields):
+    """(make_linear_shape(*fields) by reference, workspace bytes): sizes and types only."""
+    shape = make_linear_shape(*fields)
+    ref = ctypes.byref(shape)
+    return ref, int(lib().pkm_linear_workspace_size(ref, for_backward))
+
+
+def _linear_workspace(c: _Call, workspace, need: int):
     """(workspace, bytes): the caller's, or one for this call."""
     if workspace is None:
-        n = int(lib().pkm_linear_workspace_size(ctypes.byref(shape), for_backward))
-        return c.empty(max(n, 1), torch.uint8), n
+        return c.empty(max(need, 1), torch.uint8), need
     return _given_workspace(c, workspace)
 
 
@@ -759,14 +789,14 @@ def pkm_linear_forward(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Te
     out_dtype = out_dtype or x.dtype
     if pre is not None:
         _check("pre", pre, (M, N), x.dtype, dev)
-    shape = make_linear_shape(M, N, K, x.dtype, out_dtype, act)
+    ref, need = _linear_ref(0, M, N, K, x.dtype, out_dtype, act)
     with _Call(dev, stream) as c:
         if out is None:
             out = c.empty((M, N), out_dtype)
         if pre is None and want_pre:
             pre = c.empty((M, N), x.dtype)
-        ws, nbytes = _linear_workspace(c, shape, workspace, 0)
-        rc = lib().pkm_linear_forward(ctypes.byref(shape), _addr(x), _addr(W), _addr(bias),
+        ws, nbytes = _linear_workspace(c, workspace, need)
+        rc = lib().pkm_linear_forward(ref, _addr(x), _addr(W), _addr(bias),
                                       _addr(residual), _addr(out), _addr(pre),
                                       _addr(ws), nbytes, c.handle)
     if rc != PKM_OK:
@@ -797,10 +827,10 @@ def pkm_linear_backward(x: torch.Tensor, W: torch.Tensor, grad_y: torch.Tensor, 
         _check("grads['W']", gW, (N, K), torch.float32, dev)
     if gb is not None:
         _check("grads['bias']", gb, (N,), torch.float32, dev)
-    shape = make_linear_shape(M, N, K, x.dtype, x.dtype if gx is None else gx.dtype, act)
+    ref, need = _linear_ref(1, M, N, K, x.dtype, x.dtype if gx is None else gx.dtype, act)
     with _Call(dev, stream) as c:
-        ws, nbytes = _linear_workspace(c, shape, workspace, 1)
-        rc = lib().pkm_linear_backward(ctypes.byref(shape), _addr(x), _addr(W), _addr(grad_y),
+        ws, nbytes = _linear_workspace(c, workspace, need)
+        rc = lib().pkm_linear_backward(ref, _addr(x), _addr(W), _addr(grad_y),
                                        _addr(pre), _addr(gx), _addr(gW), _addr(gb),
                                        _addr(ws), nbytes, c.handle)
     if rc != PKM_OK:

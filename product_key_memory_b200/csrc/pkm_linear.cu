@@ -18,12 +18,19 @@ constexpr int kMaxSplit = 16;
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 int64_t pad8(int64_t x) { return (x + 7) / 8 * 8; }
 
+// A call's status word is cleared by its first kernel: one operation less in the stream.
+__device__ __forceinline__ void clear_status(int* status) {
+  if (status && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = 0;
+}
+
 // ---------------------------------------------------------------- small batches
 // One warp per output column: the lanes split the W row (read once, 4 accesses in flight),
 // x comes from L1/L2, the lanes' sums are added by a tree. Bound by reading W.
 template <typename E, int V, int M>
 __global__ void __launch_bounds__(256) linear_small_kernel(const void* x, const void* W, int N,
-                                                           int K, const LinearEpilogue epi) {
+                                                           int K, const LinearEpilogue epi,
+                                                           int* status) {
+  clear_status(status);
   const int lane = threadIdx.x & 31;
   const int col = blockIdx.x * 8 + (threadIdx.x >> 5);
   if (col >= N) return;
@@ -63,13 +70,13 @@ __global__ void __launch_bounds__(256) linear_small_kernel(const void* x, const 
 
 template <typename E, int V>
 cudaError_t run_small(int M, const void* x, const void* W, int N, int K,
-                      const LinearEpilogue& epi, cudaStream_t st) {
+                      const LinearEpilogue& epi, int* status, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>((N + 7) / 8);
   switch (M) {
 #define PKM_CASE(m) \
-  case m: linear_small_kernel<E, V, m><<<grid, 256, 0, st>>>(x, W, N, K, epi); break;
+  case m: linear_small_kernel<E, V, m><<<grid, 256, 0, st>>>(x, W, N, K, epi, status); break;
     PKM_CASE(1) PKM_CASE(2) PKM_CASE(3) PKM_CASE(4) PKM_CASE(5) PKM_CASE(6) PKM_CASE(7)
-    default: linear_small_kernel<E, V, 8><<<grid, 256, 0, st>>>(x, W, N, K, epi);
+    default: linear_small_kernel<E, V, 8><<<grid, 256, 0, st>>>(x, W, N, K, epi, status);
 #undef PKM_CASE
   }
   return cudaGetLastError();
@@ -126,7 +133,9 @@ __device__ __forceinline__ void store_planes(uint16_t* dst, int64_t plane, int64
 // [rows][cols] of E -> NP planes [rows][ld] of bf16, ld a multiple of 8.
 template <typename E, int V, int NP>
 __global__ void __launch_bounds__(256) linear_planes_kernel(const void* src, uint16_t* dst,
-                                                            int64_t rows, int cols, int64_t ld) {
+                                                            int64_t rows, int cols, int64_t ld,
+                                                            int* status) {
+  clear_status(status);
   const int chunks = static_cast<int>(ld / 8);
   const int64_t total = rows * chunks;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
@@ -140,16 +149,16 @@ __global__ void __launch_bounds__(256) linear_planes_kernel(const void* src, uin
 }
 
 cudaError_t make_planes(const void* src, int dtype, uint16_t* dst, int64_t rows, int cols,
-                        cudaStream_t st) {
+                        int* status, cudaStream_t st) {
   const int64_t ld = pad8(cols);
   const int64_t blocks = (rows * (ld / 8) + 255) / 256;
   const unsigned grid = static_cast<unsigned>(blocks < 148 * 32 ? blocks : 148 * 32);
   const bool vec = cols % 8 == 0;
   if (dtype == PKM_F32) {
-    if (vec) linear_planes_kernel<F32, 8, 3><<<grid, 256, 0, st>>>(src, dst, rows, cols, ld);
-    else linear_planes_kernel<F32, 1, 3><<<grid, 256, 0, st>>>(src, dst, rows, cols, ld);
+    if (vec) linear_planes_kernel<F32, 8, 3><<<grid, 256, 0, st>>>(src, dst, rows, cols, ld, status);
+    else linear_planes_kernel<F32, 1, 3><<<grid, 256, 0, st>>>(src, dst, rows, cols, ld, status);
   } else {
-    linear_planes_kernel<BF16, 1, 1><<<grid, 256, 0, st>>>(src, dst, rows, cols, ld);
+    linear_planes_kernel<BF16, 1, 1><<<grid, 256, 0, st>>>(src, dst, rows, cols, ld, status);
   }
   return cudaGetLastError();
 }
@@ -163,8 +172,10 @@ constexpr int kPrepRows = 64;
 template <typename E, int V, int NP>
 __global__ void __launch_bounds__(256) linear_slope_kernel(const void* gy, const void* pre,
                                                            int act, uint16_t* dst, float* part,
-                                                           int64_t rows, int cols, int64_t ld) {
+                                                           int64_t rows, int cols, int64_t ld,
+                                                           int* status) {
   __shared__ float sh[8][256];
+  clear_status(status);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.y * 256 + lane * 8;
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kPrepRows;
@@ -218,22 +229,26 @@ __global__ void __launch_bounds__(256) linear_bias_kernel(const float* __restric
 
 template <typename E, int V>
 cudaError_t run_slope(int planes, const void* gy, const void* pre, int act, uint16_t* dst,
-                      float* part, int64_t rows, int cols, cudaStream_t st) {
+                      float* part, int64_t rows, int cols, int* status, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>((rows + kPrepRows - 1) / kPrepRows),
                   static_cast<unsigned>((cols + 255) / 256));
   const int64_t ld = pad8(cols);
   switch (planes) {
     case 0:
-      linear_slope_kernel<E, V, 0><<<grid, 256, 0, st>>>(gy, pre, act, dst, part, rows, cols, ld);
+      linear_slope_kernel<E, V, 0><<<grid, 256, 0, st>>>(gy, pre, act, dst, part, rows, cols, ld,
+                                                          status);
       break;
     case 1:
-      linear_slope_kernel<E, V, 1><<<grid, 256, 0, st>>>(gy, pre, act, dst, part, rows, cols, ld);
+      linear_slope_kernel<E, V, 1><<<grid, 256, 0, st>>>(gy, pre, act, dst, part, rows, cols, ld,
+                                                          status);
       break;
     case 2:
-      linear_slope_kernel<E, V, 2><<<grid, 256, 0, st>>>(gy, pre, act, dst, part, rows, cols, ld);
+      linear_slope_kernel<E, V, 2><<<grid, 256, 0, st>>>(gy, pre, act, dst, part, rows, cols, ld,
+                                                          status);
       break;
     default:
-      linear_slope_kernel<E, V, 3><<<grid, 256, 0, st>>>(gy, pre, act, dst, part, rows, cols, ld);
+      linear_slope_kernel<E, V, 3><<<grid, 256, 0, st>>>(gy, pre, act, dst, part, rows, cols, ld,
+                                                          status);
   }
   return cudaGetLastError();
 }
@@ -389,33 +404,34 @@ cudaError_t launch_linear_forward(const LinearArgs& a, const void* x, const void
   LinearEpilogue epi{y, bias, residual, pre, nullptr, 0, a.out_dtype == PKM_F32,
                      a.dtype == PKM_F32, a.act};
   int* status = static_cast<int*>(workspace);
-  cudaError_t e = cudaMemsetAsync(status, 0, sizeof(int), st);
-  if (e != cudaSuccess) return e;
+  int* first = status;   // what the next kernel clears: only the call's first one does
+  cudaError_t e = cudaSuccess;
   if (linear_small(a)) {
     ++*launches;
     const int M = static_cast<int>(a.M);
     const bool vec = a.K % 8 == 0;
     if (a.dtype == PKM_F32)
-      return vec ? run_small<F32, 8>(M, x, W, a.N, a.K, epi, st)
-                 : run_small<F32, 1>(M, x, W, a.N, a.K, epi, st);
-    return vec ? run_small<BF16, 8>(M, x, W, a.N, a.K, epi, st)
-               : run_small<BF16, 1>(M, x, W, a.N, a.K, epi, st);
+      return vec ? run_small<F32, 8>(M, x, W, a.N, a.K, epi, first, st)
+                 : run_small<F32, 1>(M, x, W, a.N, a.K, epi, first, st);
+    return vec ? run_small<BF16, 8>(M, x, W, a.N, a.K, epi, first, st)
+               : run_small<BF16, 1>(M, x, W, a.N, a.K, epi, first, st);
   }
   const Layout l = layout(a, false);
   char* ws = static_cast<char*>(workspace);
   const int64_t ld = pad8(a.K);
   if (!in_place(a.dtype, a.K)) {
-    e = make_planes(x, a.dtype, reinterpret_cast<uint16_t*>(ws + l.x), a.M, a.K, st);
+    e = make_planes(x, a.dtype, reinterpret_cast<uint16_t*>(ws + l.x), a.M, a.K, first, st);
     if (e == cudaSuccess)
-      e = make_planes(W, a.dtype, reinterpret_cast<uint16_t*>(ws + l.W), a.N, a.K, st);
+      e = make_planes(W, a.dtype, reinterpret_cast<uint16_t*>(ws + l.W), a.N, a.K, nullptr, st);
     if (e != cudaSuccess) return e;
+    first = nullptr;
     x = ws + l.x;
     W = ws + l.W;
     *launches += 2;
   }
   const uint32_t in = static_cast<uint32_t>(input_planes(a.dtype));
   const LinearGemm g{kForward, l.fwd.tile, x, W, ld, ld, static_cast<int>(a.M), a.N, a.K, in, in,
-                     l.fwd_p.a, l.fwd_p.b, l.fwd_p.pairs, l.fwd.ksplit, epi, status};
+                     l.fwd_p.a, l.fwd_p.b, l.fwd_p.pairs, l.fwd.ksplit, epi, status, first != nullptr};
   return product(g, reinterpret_cast<float*>(ws + l.part), launches, st);
 }
 
@@ -426,8 +442,8 @@ cudaError_t launch_linear_backward(const LinearArgs& a, const void* x, const voi
   const Layout l = layout(a, true);
   char* ws = static_cast<char*>(workspace);
   int* status = static_cast<int*>(workspace);
-  cudaError_t e = cudaMemsetAsync(status, 0, sizeof(int), st);
-  if (e != cudaSuccess) return e;
+  int* first = status;   // what the next kernel clears: only the call's first one does
+  cudaError_t e = cudaSuccess;
   const int dp = slope_planes(a);
   const int64_t ldn = pad8(a.N), ldk = pad8(a.K);
   uint16_t* d = reinterpret_cast<uint16_t*>(ws + l.d);
@@ -437,12 +453,13 @@ cudaError_t launch_linear_backward(const LinearArgs& a, const void* x, const voi
     const int planes = want_d ? dp : 0;
     const bool vec = a.N % 8 == 0;
     if (a.dtype == PKM_F32)
-      e = vec ? run_slope<F32, 8>(planes, grad_y, pre, a.act, d, part, a.M, a.N, st)
-              : run_slope<F32, 1>(planes, grad_y, pre, a.act, d, part, a.M, a.N, st);
+      e = vec ? run_slope<F32, 8>(planes, grad_y, pre, a.act, d, part, a.M, a.N, first, st)
+              : run_slope<F32, 1>(planes, grad_y, pre, a.act, d, part, a.M, a.N, first, st);
     else
-      e = vec ? run_slope<BF16, 8>(planes, grad_y, pre, a.act, d, part, a.M, a.N, st)
-              : run_slope<BF16, 1>(planes, grad_y, pre, a.act, d, part, a.M, a.N, st);
+      e = vec ? run_slope<BF16, 8>(planes, grad_y, pre, a.act, d, part, a.M, a.N, first, st)
+              : run_slope<BF16, 1>(planes, grad_y, pre, a.act, d, part, a.M, a.N, first, st);
     if (e != cudaSuccess) return e;
+    first = nullptr;
     ++*launches;
     if (grad_bias) {
       linear_bias_kernel<<<(a.N + 31) / 32, 256, 0, st>>>(
@@ -459,28 +476,31 @@ cudaError_t launch_linear_backward(const LinearArgs& a, const void* x, const voi
   float* part = reinterpret_cast<float*>(ws + l.part);
   if (grad_x) {
     if (!inpl) {
-      e = make_planes(W, a.dtype, reinterpret_cast<uint16_t*>(ws + l.W), a.N, a.K, st);
+      e = make_planes(W, a.dtype, reinterpret_cast<uint16_t*>(ws + l.W), a.N, a.K, first, st);
       if (e != cudaSuccess) return e;
+      first = nullptr;
       W = ws + l.W;
       ++*launches;
     }
     const LinearEpilogue epi{grad_x, nullptr, nullptr, nullptr, nullptr, 0,
                              a.out_dtype == PKM_F32, 0, PKM_ACT_NONE};
     const LinearGemm g{kGradX, l.gx.tile, dop, W, ldn, ldk, static_cast<int>(a.M), a.K, a.N,
-                       dcount, in, l.gx_p.a, l.gx_p.b, l.gx_p.pairs, l.gx.ksplit, epi, status};
+                       dcount, in, l.gx_p.a, l.gx_p.b, l.gx_p.pairs, l.gx.ksplit, epi, status, first != nullptr};
     e = product(g, part, launches, st);
     if (e != cudaSuccess) return e;
+    first = nullptr;
   }
   if (grad_W) {
     if (!inpl) {
-      e = make_planes(x, a.dtype, reinterpret_cast<uint16_t*>(ws + l.x), a.M, a.K, st);
+      e = make_planes(x, a.dtype, reinterpret_cast<uint16_t*>(ws + l.x), a.M, a.K, first, st);
       if (e != cudaSuccess) return e;
+      first = nullptr;
       x = ws + l.x;
       ++*launches;
     }
     const LinearEpilogue epi{grad_W, nullptr, nullptr, nullptr, nullptr, 0, 1, 0, PKM_ACT_NONE};
     const LinearGemm g{kGradW, l.gw.tile, dop, x, ldn, ldk, a.N, a.K, static_cast<int>(a.M),
-                       dcount, in, l.gw_p.a, l.gw_p.b, l.gw_p.pairs, l.gw.ksplit, epi, status};
+                       dcount, in, l.gw_p.a, l.gw_p.b, l.gw_p.pairs, l.gw.ksplit, epi, status, first != nullptr};
     e = product(g, part, launches, st);
   }
   return e;

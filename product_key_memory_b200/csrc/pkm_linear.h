@@ -23,8 +23,8 @@ struct LinearEpilogue {
 };
 
 enum LinearLayout { kForward, kGradX, kGradW };
-// Tile shapes: 256 x 256 on a pair of CTAs, 128 x 128 and 128 x 64 on one.
-enum LinearTile { kTile256, kTile128, kTile64 };
+// Tile shapes: 256 x 256, 192 and 128 on a pair of CTAs, 128 x 128 and 128 x 64 on one.
+enum LinearTile { kTile256, kTile192, kTilePair128, kTile128, kTile64 };
 
 // One product C[M][N] over K. A: K-major [a_count][M][lda] (forward, grad_x) or MN-major
 // [a_count][K][lda] (grad_W); B: K-major [b_count][N][ldb] (forward) or MN-major
@@ -41,6 +41,7 @@ struct LinearGemm {
   int pairs, ksplit;
   LinearEpilogue epi;
   int* status;
+  int clear;   // clear the status word first
 };
 cudaError_t launch_linear_gemm(const LinearGemm& g, cudaStream_t st);
 

@@ -11,9 +11,8 @@
 // hi, mid, lo whose sum is the value to 2^-24, and the products whose size is above 2^-24
 // are added in one fp32 accumulator, the K loop running over (K block, plane pair).
 //
-// Persistent, warp-specialised, 320 threads: warp 0 TMA producer, warp 1 MMA issuer,
-// warps 2..9 epilogue (two per TMEM lane quadrant, half of the columns each), the
-// accumulator double-buffered in TMEM. A tile is CG x 128 rows by BN columns: with CG = 2
+// Persistent, warp-specialised: warp 0 TMA producer, warp 1 MMA issuer, the others
+// epilogue, the accumulator double-buffered in TMEM. A tile is CG x 128 rows by BN columns: with CG = 2
 // a pair of CTAs shares each MMA (cta_group::2), every CTA loading half of A's rows and
 // half of B's columns. Every wait is bounded as in the query kernel; the pair leaves
 // through a cluster barrier, so neither CTA exits under the other's copies or MMAs.
@@ -25,7 +24,9 @@
 // the next segment is multiplied into the other half of TMEM. Plane pairs go smallest
 // first inside a segment, so the small ones are added to small sums.
 //
-// Epilogue: a thread owns a row of 32 columns at a time. Rows go through shared memory,
+// Epilogue: with PROMOTE 8 warps (two per TMEM lane quadrant; their accumulators take the
+// registers), else up to 16, whose activations hide one another's latencies. A thread owns
+// a row of 32 columns at a time. Rows go through shared memory,
 // swizzled, and leave as TMA stores of 32 x 32 (a thread's own 16-byte stores would touch
 // a line per lane); outputs whose rows are no multiple of 16 bytes go out a row at a
 // time, lanes along the columns.
@@ -39,24 +40,28 @@ using namespace tc;
 
 namespace {
 
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kRows = 128;               // rows of a tile per CTA
 constexpr int kK = 64;                   // K per stage: one 128-byte swizzled row of bf16
-constexpr int kSegment = 4;              // K blocks between two takings (PROMOTE)
+constexpr int kSegment = 8;              // K blocks between two takings (PROMOTE)
 constexpr uint32_t kABytes = kRows * kK * 2;
 constexpr uint32_t kMnBlock = 64 * kK * 2;   // 64 MN x 64 K of an MN-major operand
-// Staging of one epilogue warp: 32 x 32 outputs of y and pre, 4 KiB of either in fp32, 2 in
-// bf16; two sets of buffers in turn where both fit twice.
-constexpr uint32_t kStaging = 8192;
 
-template <int CG, int BN> struct Tile {
+template <bool B_MN, int CG, int BN, bool PROMOTE> struct Tile {
   static constexpr int kCols = BN / CG;                      // of B per CTA
-  static constexpr uint32_t kBBytes = kCols * kK * 2;
+  static constexpr int kMnBlocks = (kCols + 63) / 64;        // an MN-major B comes in whole blocks
+  static constexpr uint32_t kBBytes = B_MN ? kMnBlocks * kMnBlock : kCols * kK * 2;
   static constexpr uint32_t kStage = kABytes + kBBytes;
   static constexpr int kStages = 163840 / kStage;            // 160 KiB of stages
-  static constexpr size_t kSmem = 1024 + kStages * kStage + kEpiWarps * kStaging + 512;
-  static constexpr uint32_t kTmemCols = 2 * BN;
+  // Epilogue warps: each takes kWide columns of its quadrant's rows.
+  static constexpr int kWide = PROMOTE ? BN / 2 : (BN >= 192 ? 64 : 32);
+  static constexpr int kEpi = 4 * (BN / kWide);
+  static constexpr int kThreads = 64 + 32 * kEpi;
+  // Staging of one epilogue warp: 32 x 32 outputs of y and pre, 4 KiB of either in fp32, 2 in
+  // bf16; two sets of buffers in turn where both fit twice. Without PROMOTE all outputs
+  // are bf16, or the parts of a split alone.
+  static constexpr uint32_t kStaging = kEpi > 8 ? 4096 : 8192;
+  static constexpr size_t kSmem = 1024 + kStages * kStage + kEpi * kStaging + 512;
+  static constexpr uint32_t kTmemCols = BN > 128 ? 512 : 2 * BN;
 };
 
 __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
@@ -80,6 +85,19 @@ __device__ __forceinline__ Step step_at(int i, int kblocks, int seg, int pairs) 
   const int here = min(seg, kblocks - s * seg);
   const int pr = r / here;
   return {s * seg + r - pr * here, pr};
+}
+
+// Tiles go in groups of kGroupM rows of tiles, down the group's rows first: the tiles in
+// flight at a time share their operands in both directions.
+constexpr int kGroupM = 8;
+struct TileAt {
+  int m, n;
+};
+__device__ __forceinline__ TileAt tile_at(int i, int mt, int nt) {
+  const int g = i / (kGroupM * nt), r = i - g * (kGroupM * nt);
+  const int rows = min(kGroupM, mt - g * kGroupM);
+  const int n = r / rows;
+  return {g * kGroupM + r - n * rows, n};
 }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
@@ -220,32 +238,32 @@ __device__ __forceinline__ void store_block(const CUtensorMap* tm_y, const CUten
     if (o.sets == 2) o.turn ^= 1;
     return;
   }
-  // Rows of any length: transposed through shared memory, 33 words a row, then a row at a
-  // time with the lanes along the columns.
+  // Rows of any length: transposed through shared memory (word i of row r at i xor r, so
+  // neither direction has bank conflicts), then a row at a time, lanes along the columns.
   const uint32_t base = o.staging;
   __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 32; ++i) sts_f32(base + (lane * 33 + i) * 4, v[i]);
+  for (int i = 0; i < 32; ++i) sts_f32(base + (lane * 32 + (i ^ lane)) * 4, v[i]);
   __syncwarp();
   if (col + lane < N) {
     const int rows = min(32, M - row0);
     for (int r = 0; r < rows; ++r)
       linear_store1(e, static_cast<int64_t>(row0 + r) * N + col + lane, col + lane,
-                    lds_f32(base + (r * 33 + lane) * 4));
+                    lds_f32(base + (r * 32 + (lane ^ r)) * 4));
   }
 }
 
 template <bool A_MN, bool B_MN, int CG, int BN, bool PROMOTE>
-__global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(
+__global__ void __launch_bounds__(Tile<B_MN, CG, BN, PROMOTE>::kThreads, 1) linear_tc_kernel(
     const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
     const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_pre, int M,
     int N, int K, uint32_t a_planes, uint32_t b_planes, int pairs, int ksplit, int use_tma,
-    const LinearEpilogue epi, int* status) {
-  using T = Tile<CG, BN>;
+    const LinearEpilogue epi, int* status, int clear) {
+  using T = Tile<B_MN, CG, BN, PROMOTE>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = align1024(smem_raw);
   uint8_t* staging = stages + T::kStages * T::kStage;
-  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStaging);
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + T::kEpi * T::kStaging);
   uint64_t* empty = full + T::kStages;
   uint64_t* tfull = empty + T::kStages;
   uint64_t* tempty = tfull + 2;
@@ -265,13 +283,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(
   const int first = blockIdx.x / CG, stride = gridDim.x / CG;
 
   if (threadIdx.x == 0) {
+    if (clear && blockIdx.x == 0) *status = 0;
     for (int s = 0; s < T::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], CG * kEpiWarps);
+      mbar_init(&tempty[b], CG * T::kEpi);
     }
     mbar_init(drain, 1);
     *abort = 0;
@@ -296,9 +315,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(
       int issued = 0;
       bool ok = true;
       for (int t = first; t < ntiles && ok; t += stride) {
-        const int sp = t % ksplit, mn = t / ksplit;
-        const int m0 = (mn / nt) * (CG * kRows) + rank * kRows;
-        const int n0 = (mn % nt) * BN + rank * T::kCols;
+        const int sp = t % ksplit;
+        const TileAt mn = tile_at(t / ksplit, mt, nt);
+        const int m0 = mn.m * (CG * kRows) + rank * kRows;
+        const int n0 = mn.n * BN + rank * T::kCols;
         const int kblocks = min(per, all - sp * per);
         for (int i = 0; i < kblocks * pairs; ++i) {
           if (!mbar_wait(&empty[s], ph ^ 1, status, abort)) { ok = false; break; }
@@ -323,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(
           }
           if (B_MN) {
 #pragma unroll
-            for (int blk = 0; blk < T::kCols / 64; ++blk)
+            for (int blk = 0; blk < T::kMnBlocks; ++blk)
               tma_load_3d_cg<CG>(b + blk * kMnBlock, &tm_b, bar, n0 + 64 * blk, k0, pb);
           } else {
             tma_load_3d_cg<CG>(b, &tm_b, bar, k0, n0, pb);
@@ -390,24 +410,25 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(
     }
   } else {
     // ---------------- epilogue: one thread per output row
-    constexpr int kGroups = BN / 64;          // groups of 32 columns per warp
+    constexpr int kGroups = T::kWide / 32;
     const int quad = warp & 3;
     const int cset = (warp - 2) >> 2;
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
     const bool part = epi.part != nullptr;
     Outputs o;
-    o.staging = smem_addr(staging + (warp - 2) * kStaging);
+    o.staging = smem_addr(staging + (warp - 2) * T::kStaging);
     o.pre_at = part || epi.y_f32 ? 4096 : 2048;
     o.set = o.pre_at + (epi.pre && !part ? (epi.pre_f32 ? 4096 : 2048) : 0);
-    o.sets = o.set * 2 <= kStaging ? 2 : 1;
+    o.sets = o.set * 2 <= T::kStaging ? 2 : 1;
     o.turn = 0;
     o.tma = use_tma;
     int it = 0;
     bool ok = true;
     for (int t = first; t < ntiles && ok; t += stride) {
-      const int sp = t % ksplit, mn = t / ksplit;
-      const int row0 = (mn / nt) * (CG * kRows) + rank * kRows + quad * 32;
-      const int n0 = (mn % nt) * BN + cset * (BN / 2);
+      const int sp = t % ksplit;
+      const TileAt mn = tile_at(t / ksplit, mt, nt);
+      const int row0 = mn.m * (CG * kRows) + rank * kRows + quad * 32;
+      const int n0 = mn.n * BN + cset * T::kWide;
       const int segments = (min(per, all - sp * per) + seg - 1) / seg;
       float acc[PROMOTE ? kGroups : 1][32];
       if (PROMOTE) {
@@ -421,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(
         const uint32_t tph = (it >> 1) & 1;
         if (!warp_wait(&tfull[buf], tph, status, abort)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + lane_addr + buf * BN + cset * (BN / 2);
+        const uint32_t d_tmem = tmem_base + lane_addr + buf * BN + cset * T::kWide;
         if (PROMOTE) {
 #pragma unroll
           for (int h = 0; h < 2 * kGroups; ++h) {
@@ -490,7 +511,7 @@ bool output_map(CUtensorMap* m, const void* p, bool f32, int64_t cols, int64_t l
 
 template <bool A_MN, bool B_MN, int CG, int BN, bool PROMOTE>
 cudaError_t run(const LinearGemm& g, cudaStream_t st) {
-  using T = Tile<CG, BN>;
+  using T = Tile<B_MN, CG, BN, PROMOTE>;
   CUtensorMap tm_a, tm_b;
   // K-major: [planes][rows][K]; MN-major: [planes][K][columns]; ld elements a row.
   const cuuint64_t al = static_cast<cuuint64_t>(g.lda) * 2, bl = static_cast<cuuint64_t>(g.ldb) * 2;
@@ -521,7 +542,7 @@ cudaError_t run(const LinearGemm& g, cudaStream_t st) {
   const int most = sm_count() / CG;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((tiles < most ? tiles : most) * CG);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(T::kThreads);
   cfg.dynamicSmemBytes = T::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -532,21 +553,22 @@ cudaError_t run(const LinearGemm& g, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = CG == 2 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, tm_a, tm_b, tm_y, tm_pre, g.M, g.N, g.K, g.a_planes,
-                            g.b_planes, g.pairs, g.ksplit, tma, g.epi, g.status);
+                            g.b_planes, g.pairs, g.ksplit, tma, g.epi, g.status, g.clear);
 }
 
 template <bool A_MN, bool B_MN, int CG, int BN>
 cudaError_t promoted(const LinearGemm& g, cudaStream_t st) {
-  // fp32 results of more than one segment; a bf16 result's own rounding hides the cuts.
-  const bool exact = g.epi.y_f32 || (g.epi.pre && g.epi.pre_f32);
-  return exact && g.K > kSegment * kK ? run<A_MN, B_MN, CG, BN, true>(g, st)
-                                      : run<A_MN, B_MN, CG, BN, false>(g, st);
+  // fp32 results; a bf16 result's own rounding hides the cuts.
+  return g.epi.y_f32 || (g.epi.pre && g.epi.pre_f32) ? run<A_MN, B_MN, CG, BN, true>(g, st)
+                                                     : run<A_MN, B_MN, CG, BN, false>(g, st);
 }
 
 template <bool A_MN, bool B_MN>
 cudaError_t pick(const LinearGemm& g, cudaStream_t st) {
   switch (g.tile) {
     case kTile256: return promoted<A_MN, B_MN, 2, 256>(g, st);
+    case kTile192: return promoted<A_MN, B_MN, 2, 192>(g, st);
+    case kTilePair128: return promoted<A_MN, B_MN, 2, 128>(g, st);
     case kTile128: return promoted<A_MN, B_MN, 1, 128>(g, st);
     default: return promoted<A_MN, B_MN, 1, 64>(g, st);
   }
