@@ -1,6 +1,6 @@
 // pkm_linear.cu -- the dense layer around its tensor-core product: the small-batch
-// forward, operand planes, the backward's d = grad_y act'(pre), column sums, and the sum
-// of a split product.
+// forward, operand planes, the backward's d = grad_y act'(pre), column sums, and how a
+// product's tiles are shared out.
 #include "pkm_linear.h"
 
 #include "pkm_block.h"
@@ -13,7 +13,6 @@ namespace pkm {
 namespace {
 
 constexpr int kSmallM = 8;          // rows of the small-batch kernel
-constexpr int kMaxSplit = 16;
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 int64_t pad8(int64_t x) { return (x + 7) / 8 * 8; }
@@ -253,59 +252,41 @@ cudaError_t run_slope(int planes, const void* gy, const void* pre, int act, uint
   return cudaGetLastError();
 }
 
-// ----------------------------------------------------------------- split products
-// Adds the `splits` parts of each element in order and applies the epilogue: a thread takes
-// four columns of a row.
-__global__ void __launch_bounds__(256) linear_finish_kernel(LinearEpilogue epi, int64_t M, int N,
-                                                            int splits) {
-  const float* part = epi.part;
-  const int quads = static_cast<int>(epi.ldp / 4);
-  const int64_t total = M * quads;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= total) return;
-  const int64_t r = i / quads;
-  const int col = static_cast<int>(i - r * quads) * 4;
-  float4 s = *reinterpret_cast<const float4*>(part + r * epi.ldp + col);
-  for (int k = 1; k < splits; ++k) {
-    const float4 t = *reinterpret_cast<const float4*>(part + (k * M + r) * epi.ldp + col);
-    s.x += t.x; s.y += t.y; s.z += t.z; s.w += t.w;
-  }
-  const float v[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (col + j < N) linear_store1(epi, r * N + col + j, col + j, v[j]);
-}
-
 // ------------------------------------------------------------------- host side
-// A product's tile and split. The pair tile reads a third less per product than the single
-// ones, so it is taken where it fills the SMs; else the largest tile that does, and where
-// none does, the smallest with K split over the idle SMs.
-struct Plan {
-  LinearTile tile;
-  int ksplit;
-};
+// How a product is shared out over the 74 pairs of CTAs of a B200 (fixed, because the
+// workspace's size depends on it). Fewer tiles than pairs: cut along K for more pairs where
+// that takes less time, counted in K steps of a tile (0.3 us): the longest range, the
+// join kernel (12), and each pair's part, written and read at about 5 TB/s (256 rows: a third).
+// 777 x 4096 -> 1024 takes 20.8 us cut and 28.5 whole, 2048 x 2048 -> 2048 27 and 19.7.
+constexpr int kPairs = 74;
+constexpr int kMinSteps = 8;      // of a range
 
-Plan plan_gemm(int64_t M, int64_t N, int64_t K, int pairs) {
-  const int64_t blocks = (K + 63) / 64;
-  const auto tiles = [&](int rows, int cols) {
-    return ((M + rows - 1) / rows) * ((N + cols - 1) / cols);
-  };
-  const int sms = 148;   // the workspace's size depends on the plan, so on sizes alone
-  if (tiles(256, 256) * 2 >= sms * 3 / 4) return {kTile256, 1};
-  if (tiles(128, 128) >= sms * 3 / 4) return {kTile128, 1};
-  const int64_t t = tiles(128, 64);
-  int64_t split = sms / t;
-  if (split > kMaxSplit) split = kMaxSplit;
-  if (split > blocks * pairs / 4) split = blocks * pairs / 4;   // at least four steps each
-  if (split > blocks) split = blocks;
-  if (split <= 1) return {kTile64, 1};
-  const int64_t per = (blocks + split - 1) / split;             // no split is empty
-  return {kTile64, static_cast<int>((blocks + per - 1) / per)};
+LinearWork share_out(int64_t M, int64_t N, int64_t K, int products) {
+  const int kblocks = static_cast<int>((K + 63) / 64);
+  const int64_t tiles = ((M + kLinearTileM - 1) / kLinearTileM) *
+                        ((N + kLinearTileN - 1) / kLinearTileN);
+  const int64_t steps = static_cast<int64_t>(kblocks) * products;   // of one tile
+  LinearWork best{static_cast<int>(tiles < kPairs ? tiles : kPairs), static_cast<int>(tiles), 0,
+                  kblocks};
+  double least = static_cast<double>(steps);
+  const double rows = M < kLinearTileM ? static_cast<double>(M) / kLinearTileM : 1.0;
+  for (int64_t ways = 2; tiles < kPairs && ways <= 32; ++ways) {
+    const int64_t pairs = ways * tiles < kPairs ? ways * tiles : kPairs;
+    // No range is empty, or too short to be worth it.
+    if (pairs > tiles * kblocks || pairs * kMinSteps > tiles * steps) break;
+    const double cost = static_cast<double>(tiles * steps) / pairs + 12 + rows * pairs / 3;
+    if (cost < least) {
+      least = cost;
+      best = {static_cast<int>(pairs), 0, static_cast<int>(tiles), kblocks};
+    }
+    if (pairs == kPairs) break;
+  }
+  return best;
 }
 
 struct PlaneSet {
   uint32_t a, b;
-  int pairs;
+  int products;
 };
 
 // The plane pairs of a product, p + q below the larger plane count, smallest first.
@@ -324,8 +305,8 @@ size_t planes_bytes(int dtype, int64_t rows, int cols) {
                                               input_planes(dtype));
 }
 
-size_t part_bytes(const Plan& p, int64_t M, int64_t N) {
-  return p.ksplit > 1 ? align256(static_cast<size_t>(p.ksplit) * M * ((N + 3) / 4 * 4) * 4) : 0;
+size_t part_bytes(const LinearWork& w) {
+  return w.cut ? static_cast<size_t>(2 * w.pairs) * kLinearTileM * kLinearTileN * 4 : 0;
 }
 
 // The backward's d: planes written (0: grad_y itself is the operand).
@@ -337,7 +318,7 @@ int slope_planes(const LinearArgs& a) {
 
 struct Layout {
   size_t x, W, d, part, bias, total;   // offsets; total = bytes
-  Plan fwd, gx, gw;
+  LinearWork fwd, gx, gw;
   PlaneSet fwd_p, gx_p, gw_p;
 };
 
@@ -352,16 +333,16 @@ Layout layout(const LinearArgs& a, bool backward) {
   l.part = off;
   if (!backward) {
     l.fwd_p = plane_pairs(in, in);
-    l.fwd = plan_gemm(a.M, a.N, a.K, l.fwd_p.pairs);
-    off += part_bytes(l.fwd, a.M, a.N);
+    l.fwd = share_out(a.M, a.N, a.K, l.fwd_p.products);
+    off += part_bytes(l.fwd);
   } else {
     const int d = slope_planes(a);
     // grad_x in bf16: d's rounding to bf16 is no larger than grad_x's own, one plane will do.
     l.gx_p = plane_pairs(d == 2 && a.out_dtype == PKM_BF16 ? 1 : (d ? d : 1), in);
     l.gw_p = plane_pairs(d ? d : 1, in);
-    l.gx = plan_gemm(a.M, a.K, a.N, l.gx_p.pairs);
-    l.gw = plan_gemm(a.N, a.K, a.M, l.gw_p.pairs);
-    const size_t px = part_bytes(l.gx, a.M, a.K), pw = part_bytes(l.gw, a.N, a.K);
+    l.gx = share_out(a.M, a.K, a.N, l.gx_p.products);
+    l.gw = share_out(a.N, a.K, a.M, l.gw_p.products);
+    const size_t px = part_bytes(l.gx), pw = part_bytes(l.gw);
     off += px > pw ? px : pw;    // the two products run one after the other
     l.d = off;
     off += align256(static_cast<size_t>(a.M) * pad8(a.N) * 2 * d);
@@ -370,23 +351,6 @@ Layout layout(const LinearArgs& a, bool backward) {
   }
   l.total = off;
   return l;
-}
-
-// A product and, when it is split, the pass that adds the parts.
-cudaError_t product(LinearGemm g, float* part, int* launches, cudaStream_t st) {
-  if (g.ksplit > 1) {
-    g.epi.part = part;
-    g.epi.ldp = (static_cast<int64_t>(g.N) + 3) / 4 * 4;
-  }
-  cudaError_t e = launch_linear_gemm(g, st);
-  if (e != cudaSuccess) return e;
-  ++*launches;
-  if (g.ksplit == 1) return cudaSuccess;
-  const int64_t total = static_cast<int64_t>(g.M) * (g.epi.ldp / 4);
-  linear_finish_kernel<<<static_cast<unsigned>((total + 255) / 256), 256, 0, st>>>(g.epi, g.M, g.N,
-                                                                                 g.ksplit);
-  ++*launches;
-  return cudaGetLastError();
 }
 
 }  // namespace
@@ -401,7 +365,7 @@ size_t linear_workspace_bytes(const LinearArgs& a, bool backward) {
 cudaError_t launch_linear_forward(const LinearArgs& a, const void* x, const void* W,
                                   const float* bias, const void* residual, void* y, void* pre,
                                   void* workspace, int* launches, cudaStream_t st) {
-  LinearEpilogue epi{y, bias, residual, pre, nullptr, 0, a.out_dtype == PKM_F32,
+  LinearEpilogue epi{y, bias, residual, pre, a.out_dtype == PKM_F32,
                      a.dtype == PKM_F32, a.act};
   int* status = static_cast<int*>(workspace);
   int* first = status;   // what the next kernel clears: only the call's first one does
@@ -430,9 +394,11 @@ cudaError_t launch_linear_forward(const LinearArgs& a, const void* x, const void
     *launches += 2;
   }
   const uint32_t in = static_cast<uint32_t>(input_planes(a.dtype));
-  const LinearGemm g{kForward, l.fwd.tile, x, W, ld, ld, static_cast<int>(a.M), a.N, a.K, in, in,
-                     l.fwd_p.a, l.fwd_p.b, l.fwd_p.pairs, l.fwd.ksplit, epi, status, first != nullptr};
-  return product(g, reinterpret_cast<float*>(ws + l.part), launches, st);
+  const LinearGemm g{kForward, x, W, ld, ld, static_cast<int>(a.M), a.N, a.K, in, in, l.fwd_p.a,
+                     l.fwd_p.b, l.fwd_p.products, l.fwd,
+                     l.fwd.cut ? reinterpret_cast<float*>(ws + l.part) : nullptr, epi, status,
+                     first != nullptr};
+  return launch_linear_gemm(g, launches, st);
 }
 
 cudaError_t launch_linear_backward(const LinearArgs& a, const void* x, const void* W,
@@ -482,11 +448,12 @@ cudaError_t launch_linear_backward(const LinearArgs& a, const void* x, const voi
       W = ws + l.W;
       ++*launches;
     }
-    const LinearEpilogue epi{grad_x, nullptr, nullptr, nullptr, nullptr, 0,
-                             a.out_dtype == PKM_F32, 0, PKM_ACT_NONE};
-    const LinearGemm g{kGradX, l.gx.tile, dop, W, ldn, ldk, static_cast<int>(a.M), a.K, a.N,
-                       dcount, in, l.gx_p.a, l.gx_p.b, l.gx_p.pairs, l.gx.ksplit, epi, status, first != nullptr};
-    e = product(g, part, launches, st);
+    const LinearEpilogue epi{grad_x, nullptr, nullptr, nullptr, a.out_dtype == PKM_F32, 0,
+                             PKM_ACT_NONE};
+    const LinearGemm g{kGradX, dop, W, ldn, ldk, static_cast<int>(a.M), a.K, a.N, dcount, in,
+                       l.gx_p.a, l.gx_p.b, l.gx_p.products, l.gx, l.gx.cut ? part : nullptr, epi,
+                       status, first != nullptr};
+    e = launch_linear_gemm(g, launches, st);
     if (e != cudaSuccess) return e;
     first = nullptr;
   }
@@ -498,10 +465,11 @@ cudaError_t launch_linear_backward(const LinearArgs& a, const void* x, const voi
       x = ws + l.x;
       ++*launches;
     }
-    const LinearEpilogue epi{grad_W, nullptr, nullptr, nullptr, nullptr, 0, 1, 0, PKM_ACT_NONE};
-    const LinearGemm g{kGradW, l.gw.tile, dop, x, ldn, ldk, a.N, a.K, static_cast<int>(a.M),
-                       dcount, in, l.gw_p.a, l.gw_p.b, l.gw_p.pairs, l.gw.ksplit, epi, status, first != nullptr};
-    e = product(g, part, launches, st);
+    const LinearEpilogue epi{grad_W, nullptr, nullptr, nullptr, 1, 0, PKM_ACT_NONE};
+    const LinearGemm g{kGradW, dop, x, ldn, ldk, a.N, a.K, static_cast<int>(a.M), dcount, in,
+                       l.gw_p.a, l.gw_p.b, l.gw_p.products, l.gw, l.gw.cut ? part : nullptr, epi,
+                       status, first != nullptr};
+    e = launch_linear_gemm(g, launches, st);
   }
   return e;
 }

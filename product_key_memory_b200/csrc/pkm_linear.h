@@ -10,40 +10,51 @@
 
 namespace pkm {
 
-// What becomes of an output element v: pre = v + bias, y = act(pre) + residual; with `part`
-// the raw v is kept for linear_finish instead ([split][M][ldp] fp32).
+// What becomes of an output element v: pre = v + bias, y = act(pre) + residual.
 struct LinearEpilogue {
   void* y;
   const float* bias;
   const void* residual;   // y's type
   void* pre;
-  float* part;
-  int64_t ldp;
   int y_f32, pre_f32, act;
 };
 
 enum LinearLayout { kForward, kGradX, kGradW };
-// Tile shapes: 256 x 256, 192 and 128 on a pair of CTAs, 128 x 128 and 128 x 64 on one.
-enum LinearTile { kTile256, kTile192, kTilePair128, kTile128, kTile64 };
+constexpr int kLinearTileM = 256, kLinearTileN = 256;   // of a pair of CTAs
+
+// How a product's tiles are shared out over `pairs` pairs of CTAs: the first `whole` tiles go
+// round; the K blocks of the `cut` tiles after them, end to end, are dealt in equal ranges.
+struct LinearWork {
+  int pairs, whole, cut, kblocks;
+  // First K block of pair c's range.
+  __host__ __device__ int64_t begin(int c) const {
+    return static_cast<int64_t>(cut) * kblocks * c / pairs;
+  }
+  // The pair whose range holds K block p: the largest c with begin(c) <= p.
+  __host__ __device__ int owner(int64_t p) const {
+    return static_cast<int>(((p + 1) * pairs - 1) / (static_cast<int64_t>(cut) * kblocks));
+  }
+};
 
 // One product C[M][N] over K. A: K-major [a_count][M][lda] (forward, grad_x) or MN-major
 // [a_count][K][lda] (grad_W); B: K-major [b_count][N][ldb] (forward) or MN-major
-// [b_count][K][ldb]. Plane pair i of the sum is A's nibble i of a_planes with B's nibble i
-// of b_planes. Leading dimensions are multiples of 8.
+// [b_count][K][ldb]. The sum runs over `products` plane pairs, pair i being A's nibble i of
+// a_planes with B's nibble i of b_planes. Leading dimensions are multiples of 8.
 struct LinearGemm {
   LinearLayout layout;
-  LinearTile tile;
   const void *a, *b;
   int64_t lda, ldb;
   int M, N, K;
   uint32_t a_count, b_count;
   uint32_t a_planes, b_planes;
-  int pairs, ksplit;
+  int products;
+  LinearWork work;
+  float* part;     // [2 pairs][256][256] fp32 when tiles are cut, else NULL
   LinearEpilogue epi;
   int* status;
   int clear;   // clear the status word first
 };
-cudaError_t launch_linear_gemm(const LinearGemm& g, cudaStream_t st);
+cudaError_t launch_linear_gemm(const LinearGemm& g, int* launches, cudaStream_t st);
 
 struct LinearArgs {
   int64_t M;

@@ -81,4 +81,37 @@ __device__ __forceinline__ void linear_store1(const LinearEpilogue& e, int64_t a
   }
 }
 
+// Eight consecutive columns of one row; `at` and `col` are multiples of 8.
+__device__ __forceinline__ void linear_store8(const LinearEpilogue& e, int64_t at, int col,
+                                              float* v) {
+  if (e.bias) {
+    float b[8];
+    load_param<8>(e.bias, col, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += b[i];
+  }
+  if (e.pre) {
+    if (e.pre_f32) Out<F32, 8>::store(e.pre, at, v);
+    else Out<BF16, 8>::store(e.pre, at, v);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = act_value(v[i], e.act);
+  if (e.residual) {
+    float r[8];
+    if (e.y_f32) {
+      Raw<F32, 8> q;
+      q.load(e.residual, at);
+      q.get(r);
+    } else {
+      Raw<BF16, 8> q;
+      q.load(e.residual, at);
+      q.get(r);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += r[i];
+  }
+  if (e.y_f32) Out<F32, 8>::store(e.y, at, v);
+  else Out<BF16, 8>::store(e.y, at, v);
+}
+
 }  // namespace pkm

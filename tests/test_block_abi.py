@@ -202,11 +202,14 @@ def test_linear_workspace_holds_the_planes():
     used in place."""
     def size(back, **kw):
         return int(P.lib().pkm_linear_workspace_size(ctypes.byref(_linear(**kw)), back))
-    big = dict(M=4096, N=4096, K=1024)
-    assert size(0, **big) == 256
-    assert size(0, dtype=0, **big) == 256 + 3 * 2 * (4096 + 4096) * 1024
-    assert size(0, M=4096, N=4096, K=1001) == 256 + 2 * (4096 + 4096) * 1008
-    assert size(1, activation=2, **big) >= 2 * 2 * 4096 * 4096
+    even = dict(M=9472, N=512)            # 74 tiles of 256 x 256: one for each pair of CTAs
+    assert size(0, K=1024, **even) == 256
+    assert size(0, dtype=0, K=1024, **even) == 256 + 3 * 2 * (9472 + 512) * 1024
+    assert size(0, K=1001, **even) == 256 + 2 * (9472 + 512) * 1008
+    assert size(1, activation=2, K=1024, **even) >= 2 * 2 * 9472 * 512
+    # few tiles: cut along K, two fp32 parts of 256 x 256 for each pair that has a range
+    cut = size(0, M=256, N=256, K=6400) - 256
+    assert cut and cut % (2 * 256 * 256 * 4) == 0 and cut <= 74 * 2 * 256 * 256 * 4
 
 
 def test_linear_binding_checks_tensors():
