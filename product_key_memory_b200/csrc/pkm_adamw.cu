@@ -9,9 +9,14 @@
 // block takes units b, b + grid, ... and finds a unit's tensor by its first unit. A
 // warp owns 256 consecutive elements, 8 per lane, which is also the block that shares
 // a scale of 8-bit states: its largest magnitude is one warp reduction of the fp32 bits
-// (ordered like the magnitudes, NaN above all). m, v, r and their 8-bit forms are
+// (ordered like the magnitudes, NaN above all). m, v, the codes of m and the scales are
 // computed in single operations rounded to nearest (no fused multiply-add), so they are
 // the same bits as the formula evaluated step by step in fp32.
+//
+// With 8-bit states an element has 12 to 22 bytes and the arithmetic comes near the issue
+// rate, so it is kept short: a code's scale is folded into beta (powers of two: exact), an
+// element's root and quotient are the special function unit's (2^-23; only the block's
+// largest root, which decides the scale, is rounded exactly).
 #include <cuda_fp8.h>
 
 #include <math.h>
@@ -79,16 +84,33 @@ __device__ __forceinline__ float inverse_pow2(uint32_t sbits) {
   return sbits == 0x7fc00000u ? __uint_as_float(sbits) : __uint_as_float((254u << 23) - sbits);
 }
 
-__device__ __forceinline__ void widen8(uint2 codes, float scale, float* f) {
+__device__ __forceinline__ void widen8(uint2 codes, float* f) {
   const uint32_t w[2] = {codes.x, codes.y};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
         static_cast<__nv_fp8x2_storage_t>(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
     const float2 x = __half22float2(__half2(h));
-    f[2 * i] = __fmul_rn(x.x, scale);
-    f[2 * i + 1] = __fmul_rn(x.y, scale);
+    f[2 * i] = x.x;
+    f[2 * i + 1] = x.y;
   }
+}
+
+__device__ __forceinline__ float sqrt_fast(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// max(a, |b|), NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(fabsf(b)));
+  return y;
 }
 
 __device__ __forceinline__ uint2 narrow8(const float* f) {
@@ -212,15 +234,21 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     void* carrier = (fl & kMaster) ? static_cast<void*>(T.master) : T.param;
     const bool whole = i + 8 <= n;
     float p[8], g[8], m[8], v[8];
+    // 8-bit states: m and v (r then) hold the codes, their scales are in these factors.
+    float bm = list.b1, bv = list.b2;
+    if (eight) {
+      const float ms = T.ms[block], vs = T.vs[block];
+      bm *= ms;
+      bv *= vs * vs;
+    }
     if (whole) {
       const Eight rg = load8(T.grad, i, gb);
       const Eight rp = load8(carrier, i, pb);
       if (eight) {
         const uint2 rm = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(T.m) + i));
         const uint2 rv = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(T.v) + i));
-        const float ms = T.ms[block], vs = T.vs[block];
-        widen8(rm, ms, m);
-        widen8(rv, vs, v);
+        widen8(rm, m);
+        widen8(rv, v);
       } else {
         const Eight rm = load8(T.m, i, false), rv = load8(T.v, i, false);
         widen(rm, false, m);
@@ -229,7 +257,6 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       widen(rg, gb, g);
       widen(rp, pb, p);
     } else {
-      const float ms = eight ? T.ms[block] : 0.f, vs = eight ? T.vs[block] : 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const bool in = i + j < n;
@@ -238,8 +265,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         if (eight) {
           const uint32_t cm = in ? static_cast<const uint8_t*>(T.m)[i + j] : 0u;
           const uint32_t cv = in ? static_cast<const uint8_t*>(T.v)[i + j] : 0u;
-          m[j] = __fmul_rn(__half2float(__half(__nv_cvt_fp8_to_halfraw(cm, __NV_E4M3))), ms);
-          v[j] = __fmul_rn(__half2float(__half(__nv_cvt_fp8_to_halfraw(cv, __NV_E4M3))), vs);
+          m[j] = __half2float(__half(__nv_cvt_fp8_to_halfraw(cm, __NV_E4M3)));
+          v[j] = __half2float(__half(__nv_cvt_fp8_to_halfraw(cv, __NV_E4M3)));
         } else {
           m[j] = in ? static_cast<const float*>(T.m)[i + j] : 0.f;
           v[j] = in ? static_cast<const float*>(T.v)[i + j] : 0.f;
@@ -252,23 +279,24 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       keep = 1.f - mine * keep;
       step = mine * over;
     }
-    uint32_t most_m = 0, most_r = 0;
+    float most_m = 0.f, most_v = 0.f;
     float r[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float gj = __fmul_rn(g[j], grad_scale);
-      if (eight) v[j] = __fmul_rn(v[j], v[j]);
-      m[j] = __fadd_rn(__fmul_rn(list.b1, m[j]), __fmul_rn(list.c1, gj));
-      v[j] = __fadd_rn(__fmul_rn(list.b2, v[j]), __fmul_rn(__fmul_rn(list.c2, gj), gj));
-      r[j] = __fsqrt_rn(v[j]);
-      p[j] = p[j] * keep - step * (m[j] / fmaf(r[j], root, list.eps));
-      most_m = max(most_m, __float_as_uint(m[j]) & 0x7fffffffu);
-      most_r = max(most_r, __float_as_uint(r[j]) & 0x7fffffffu);
+      if (eight) v[j] = __fmul_rn(v[j], v[j]);           // of a code: exact
+      m[j] = __fadd_rn(__fmul_rn(bm, m[j]), __fmul_rn(list.c1, gj));
+      v[j] = __fadd_rn(__fmul_rn(bv, v[j]), __fmul_rn(__fmul_rn(list.c2, gj), gj));
+      r[j] = sqrt_fast(v[j]);
+      p[j] = p[j] * keep - step * (m[j] * rcp_fast(fmaf(r[j], root, list.eps)));
+      most_m = max_nan(most_m, m[j]);
+      most_v = max_nan(most_v, v[j]);
     }
     if (eight) {
-      const uint32_t bm = scale_bits(__reduce_max_sync(0xffffffffu, most_m));
-      const uint32_t br = scale_bits(__reduce_max_sync(0xffffffffu, most_r));
-      const float im = inverse_pow2(bm), ir = inverse_pow2(br);
+      const uint32_t sm = scale_bits(__reduce_max_sync(0xffffffffu, __float_as_uint(most_m)));
+      const uint32_t sr = scale_bits(__float_as_uint(__fsqrt_rn(
+          __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most_v))))) & 0x7fffffffu);
+      const float im = inverse_pow2(sm), ir = inverse_pow2(sr);
       const uint32_t key = mix32(key0 ^ T.key);
       const uint32_t pair = static_cast<uint32_t>(i >> 1);
 #pragma unroll
@@ -281,8 +309,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       }
       const uint2 cm = narrow8(m), cv = narrow8(v);
       if (lane == 0) {
-        T.ms[block] = __uint_as_float(bm);
-        T.vs[block] = __uint_as_float(br);
+        T.ms[block] = __uint_as_float(sm);
+        T.vs[block] = __uint_as_float(sr);
       }
       if (whole) {
         __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(T.m) + i), cm);

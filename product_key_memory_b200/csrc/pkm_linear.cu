@@ -91,24 +91,31 @@ __device__ __forceinline__ void split(float v, float* p) {
   p[2] = fine ? rounded<BF16>(v - p[0] - p[1]) : 0.f;
 }
 
-template <typename E, int V>
-__device__ __forceinline__ void load_cols(const void* p, int64_t at, int col, int cols, float* f) {
-  if (V == 8) {
-    Raw<E, 8> r;
-    r.load(p, at);
-    r.get(f);
-  } else {
+// Eight columns of a row from `col` (a multiple of 8) as loaded; columns from `cols` on are 0.
+// V = 8: the row is 16-byte aligned and the eight exist.
+template <typename E, int V> struct Chunk;
+template <typename E> struct Chunk<E, 8> {
+  Raw<E, 8> r;
+  __device__ __forceinline__ void load(const void* p, int64_t at, int, int) { r.load(p, at); }
+  __device__ __forceinline__ void get(float* f) const { r.get(f); }
+};
+template <typename E> struct Chunk<E, 1> {
+  Raw<E, 1> r[8];
+  int n;
+  __device__ __forceinline__ void load(const void* p, int64_t at, int col, int cols) {
+    n = cols - col;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) r[j].load(p, at + j);
+  }
+  __device__ __forceinline__ void get(float* f) const {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       f[j] = 0.f;
-      if (col + j < cols) {
-        Raw<E, 1> r;
-        r.load(p, at + j);
-        r.get(f + j);
-      }
+      if (j < n) r[j].get(f + j);
     }
   }
-}
+};
 
 template <int NP>
 __device__ __forceinline__ void store_planes(uint16_t* dst, int64_t plane, int64_t at,
@@ -142,7 +149,9 @@ __global__ void __launch_bounds__(256) linear_planes_kernel(const void* src, uin
     const int64_t r = i / chunks;
     const int col = static_cast<int>(i - r * chunks) * 8;
     float f[8];
-    load_cols<E, V>(src, r * cols + col, col, cols, f);
+    Chunk<E, V> c;
+    c.load(src, r * cols + col, col, cols);
+    c.get(f);
     store_planes<NP>(dst, rows * ld, r * ld + col, f);
   }
 }
@@ -167,6 +176,7 @@ cudaError_t make_planes(const void* src, int dtype, uint16_t* dst, int64_t rows,
 // written as NP planes (NP = 0: not needed) and its column sums as one partial row per block
 // row (part NULL: not needed).
 constexpr int kPrepRows = 64;
+constexpr int kDeep = 4;           // rows in flight per thread
 
 template <typename E, int V, int NP>
 __global__ void __launch_bounds__(256) linear_slope_kernel(const void* gy, const void* pre,
@@ -181,18 +191,30 @@ __global__ void __launch_bounds__(256) linear_slope_kernel(const void* gy, const
   float sum[8] = {};
   if (col < cols) {
     const int64_t r1 = r0 + kPrepRows < rows ? r0 + kPrepRows : rows;
-    for (int64_t r = r0 + warp; r < r1; r += 8) {
-      float g[8];
-      load_cols<E, V>(gy, r * cols + col, col, cols, g);
-      if (act != PKM_ACT_NONE) {
-        float t[8];
-        load_cols<E, V>(pre, r * cols + col, col, cols, t);
+    for (int64_t r = r0 + warp; r < r1; r += 8 * kDeep) {
+      float g[kDeep][8], t[kDeep][8];
+      Chunk<E, V> gc[kDeep], tc[kDeep];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] *= act_slope(t[j], act);
+      for (int u = 0; u < kDeep; ++u) {
+        const int64_t q = r + 8 * u;
+        if (q >= r1) continue;
+        gc[u].load(gy, q * cols + col, col, cols);
+        if (act != PKM_ACT_NONE) tc[u].load(pre, q * cols + col, col, cols);
       }
-      if (NP > 0) store_planes<NP>(dst, rows * ld, r * ld + col, g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[j] += g[j];
+      for (int u = 0; u < kDeep; ++u) {
+        const int64_t q = r + 8 * u;
+        if (q >= r1) continue;
+        gc[u].get(g[u]);
+        if (act != PKM_ACT_NONE) {
+          tc[u].get(t[u]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) g[u][j] *= act_slope(t[u][j], act);
+        }
+        if (NP > 0) store_planes<NP>(dst, rows * ld, q * ld + col, g[u]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += g[u][j];
+      }
     }
   }
   if (!part) return;

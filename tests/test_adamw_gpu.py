@@ -1,5 +1,6 @@
 """AdamW over lists of tensors on the GPU: states bit for bit against the formula evaluated step by
-step in fp32 (codes and scales of 8-bit states included), parameters against 64 bits within
+step in fp32 (codes and scales of 8-bit states included, but for second moments within the
+root's error of the middle of two codes), parameters against 64 bits within
 the roundings counted in block_ref.adamw."""
 import pytest
 import torch
@@ -52,7 +53,10 @@ def _check(t, before, hyper, index, zero=False):
     want = adamw(before, hyper, index)
     for k in ("m", "v", "m_scale", "v_scale"):
         if k in want:
-            assert _equal(t[k], want[k]), "%s of tensor %d (n %d)" % (k, index, t[k].numel())
+            same = (_bits(t[k]) == _bits(want[k])) | (t[k].float().isnan() & want[k].float().isnan())
+            if k == "v" and "v_edge" in want:
+                same |= want["v_edge"] & ((_bits(t[k]).int() - _bits(want[k]).int()).abs() <= 1)
+            assert bool(same.all()), "%s of tensor %d (n %d)" % (k, index, t[k].numel())
     if t.get("master") is not None:
         assert_within("master", t["master"], want["param"], want["bound"])
         assert torch.equal(t["param"], t["master"].to(t["param"].dtype))
@@ -120,8 +124,8 @@ def test_mixed_long_list():
 def test_extreme_values_in_8_bits():
     """Blocks of zeros, of one value, at the scales' borders, of tiny and of huge values."""
     import product_key_memory_b200 as P
-    t, _ = _tensor(P, 256 * 12, F32, F32, 8, fresh=True)
-    g = t["grad"].view(12, 256)
+    t, _ = _tensor(P, 256 * 13, F32, F32, 8, fresh=True)
+    g = t["grad"].view(13, 256)
     g[0] = 0
     g[1] = 1.0
     g[2] *= 1e-30
@@ -140,7 +144,7 @@ def test_extreme_values_in_8_bits():
         before = _copy(t)
         P.pkm_adamw_step(lst, **dict(HYPER, step=step))
         _check(t, before, dict(HYPER, step=step), 0)
-    assert bool((t["param"].view(12, 256)[0] == 0).logical_not().all())   # decay only, no NaN
+    assert bool((t["param"].view(13, 256)[0] == 0).logical_not().all())   # decay only, no NaN
     assert bool(t["param"].isfinite().all())
 
 
