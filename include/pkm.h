@@ -446,8 +446,8 @@ typedef struct {
  * keeps the codes' grid where it is from one step to the next, so writing an unchanged
  * value again is exact. m / s is rounded to nearest even. One step moves r by a small part
  * of a code, which rounding to nearest would drop every time: q = r / s is rounded to a
- * multiple of ulp, the code spacing at q, after a dither: fl(q + u ulp) to the nearest
- * multiple, with u = (b - 32767.5) / 65536, b the 16 low (even elements) or high (odd
+ * multiple of ulp, the code spacing at q, after a dither: q / ulp + u to the nearest
+ * integer, with u = (b - 32767.5) / 65536, b the 16 low (even elements) or high (odd
  * elements) bits of mix(i / 2 xor key), key = mix(mix(seed + 0x9e3779b9 t) xor
  * 0x9e3779b9 index), index the tensor's place in the list, mix MurmurHash3's 32-bit
  * finaliser, all modulo 2^32. What is above 0 stays at least the smallest code, 2^-9. All

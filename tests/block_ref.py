@@ -126,7 +126,7 @@ def adamw(t, hyper, index):
     h = mix32((i // 2) ^ key)
     b = torch.where(i % 2 == 0, h & 0xffff, h >> 16).double()
     ulp = torch.ldexp(torch.ones_like(b), (torch.frexp(q.double())[1] - 1).clamp(min=-6) - 3)
-    raw = (q + (ulp * (b - 32767.5) / 65536).float()).double()
+    raw = q.double() + ulp * (b - 32767.5) / 65536
     near = ((raw / ulp).round() * ulp).clamp(min=2.0 ** -9)
     out["v"] = torch.where(q > 0, near.float(), q).to(torch.float8_e4m3fn)
     # The kernel's root is good to 2^-22: 2^-18 of a code at most (16 steps an octave), so a
