@@ -125,32 +125,7 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
   return y;
 }
 
-// Two fp32 values and their operations, each rounded to nearest.
-struct Pair {
-  unsigned long long v;
-  __device__ __forceinline__ Pair() {}
-  __device__ __forceinline__ Pair(float a, float b) {
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
-  }
-  __device__ __forceinline__ explicit Pair(float a) : Pair(a, a) {}
-  __device__ __forceinline__ float lo() const { return get().x; }
-  __device__ __forceinline__ float hi() const { return get().y; }
-  __device__ __forceinline__ float2 get() const {
-    float2 f;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-    return f;
-  }
-};
-__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
-  Pair r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
-  Pair r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) { return mul(a, b); }
 // One at a time: the compiler fuses an addition of pairs with the product before it.
 __device__ __forceinline__ Pair operator+(Pair a, Pair b) {
   const float2 x = a.get(), y = b.get();
@@ -208,16 +183,8 @@ struct Eight {
   uint4 a, b;
 };
 
-// Streaming loads in program order: all of an element group's loads are in flight before
-// the first is used (the compiler would move some behind the arithmetic on others).
-__device__ __forceinline__ uint4 load16(const void* p) {
-  uint4 r;
-  asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p)
-               : "memory");
-  return r;
-}
+// Codes of eight elements; as load16, in program order: all of an element group's loads are
+// in flight before the first is used.
 __device__ __forceinline__ uint2 load_codes(const void* p, int64_t i) {
   uint2 r;
   asm volatile("ld.global.cs.v2.u32 {%0, %1}, [%2];"

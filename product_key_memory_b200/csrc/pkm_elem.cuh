@@ -1,5 +1,5 @@
 // pkm_elem.cuh -- typed vector loads and stores of the transformer-block kernels: V
-// consecutive elements (8: 16-byte accesses, 1: any alignment) of fp32 or bf16 arrays,
+// consecutive elements (8 and 4: 16-byte accesses to fp32, 16 and 8 to bf16; 1: any alignment) of fp32 or bf16 arrays,
 // widened to fp32. Loads are ordinary (not the read-only path): several operators may
 // run in place.
 #pragma once
@@ -45,6 +45,25 @@ template <> struct Raw<BF16, 8> {
   }
   __device__ __forceinline__ void get(float* f) const { Vec<uint16_t>::widen(a, f); }
 };
+template <> struct Raw<F32, 4> {
+  float4 a;
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    a = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+  }
+};
+template <> struct Raw<BF16, 4> {
+  uint2 a;
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    a = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i));
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    f[0] = bf16_lo(a.x); f[1] = bf16_hi(a.x);
+    f[2] = bf16_lo(a.y); f[3] = bf16_hi(a.y);
+  }
+};
 template <> struct Raw<F32, 1> {
   float a;
   __device__ __forceinline__ void load(const void* p, int64_t i) {
@@ -77,6 +96,17 @@ template <> struct Out<BF16, 8> {
                    pack_bf16(f[6], f[7]));
   }
 };
+template <> struct Out<F32, 4> {
+  __device__ __forceinline__ static void store(void* p, int64_t i, const float* f) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(f[0], f[1], f[2], f[3]);
+  }
+};
+template <> struct Out<BF16, 4> {
+  __device__ __forceinline__ static void store(void* p, int64_t i, const float* f) {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) =
+        make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
+  }
+};
 template <> struct Out<F32, 1> {
   __device__ __forceinline__ static void store(void* p, int64_t i, const float* f) {
     static_cast<float*>(p)[i] = f[0];
@@ -96,9 +126,56 @@ __device__ __forceinline__ void load_param(const float* p, int i, float* f) {
     const float4 b = __ldg(reinterpret_cast<const float4*>(p + i) + 1);
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  } else if (V == 4) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p + i));
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
   } else {
     f[0] = __ldg(p + i);
   }
+}
+
+// A streaming load that stays where it is written: loads meant to be in flight together or
+// ahead of their use are not moved behind other arithmetic.
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
+// Two fp32 values and their operations (one instruction for both), each rounded to nearest.
+struct Pair {
+  unsigned long long v;
+  Pair() = default;
+  __device__ __forceinline__ Pair(float a, float b) {
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  }
+  __device__ __forceinline__ explicit Pair(float a) : Pair(a, a) {}
+  __device__ __forceinline__ float lo() const { return get().x; }
+  __device__ __forceinline__ float hi() const { return get().y; }
+  __device__ __forceinline__ float2 get() const {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+  }
+};
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+// May be fused with a product before it.
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
 }
 
 // The value as an array of type E holds it.

@@ -12,120 +12,110 @@
 // rows in a fixed order.
 #include "pkm_block.h"
 #include "pkm_elem.cuh"
+#include "pkm_kernels.h"
 #include "pkm_tc.h"
 
 namespace pkm {
 
 namespace {
 
-// Sum over the T threads of a row (T a power of two up to 32, or a multiple of 32 that
-// is the whole block). `red` holds one float per warp and is reused: callers alternate.
-template <bool BLK>
-__device__ __forceinline__ float row_sum(float v, int T, float* red) {
-  const int w = BLK ? 32 : T;
-  for (int o = w >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (BLK) {
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
+constexpr int kMaxNormThreads = 512;
+
+// Barrier of the `threads` threads of group g of a block (whole warps).
+__device__ __forceinline__ void group_barrier(int g, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(threads) : "memory");
+}
+
+// Sum over the lanes of a row and its warps; `red` holds a float for each of those. Callers take
+// turns with two arrays.
+template <int LANES>
+__device__ __forceinline__ float row_sum(float v, int wide, int group, int w, float* red) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (wide > 1) {
+    if ((threadIdx.x & 31) == 0) red[w] = v;
+    group_barrier(group, wide * 32);
     v = 0.f;
-    for (int i = 0; i < (T >> 5); ++i) v += red[i];
+    for (int i = 0; i < wide; ++i) v += red[i];
   }
   return v;
 }
 
-constexpr int kMaxNormThreads = 512;
-
-// V elements per access, C accesses per thread: thread t of a row holds the elements
-// (c T + t) V ... + V - 1 for c < C.
-template <typename X, typename Y, int V, int C, bool BLK>
-__global__ void __launch_bounds__(BLK ? kMaxNormThreads : 256)
+// V = 4: rows of a multiple of 4 columns, four at a time, contiguous over the lanes. V = 1: any.
+// A row belongs to LANES lanes of `wide` warps (1 where LANES < 32), H accesses each.
+template <typename X, typename Y, int V, int H, int LANES>
+__global__ void __launch_bounds__(kMaxNormThreads)
 layernorm_forward_kernel(const void* x, const void* add, int add_f32,
                          const float* __restrict__ gamma, const float* __restrict__ beta, void* y,
-                         void* sum, float* mean_out, float* rstd_out, int64_t rows, int d, int T,
+                         void* sum, float* mean_out, float* rstd_out, int64_t rows, int d, int wide,
                          float eps) {
   __shared__ float red[2][kMaxNormThreads / 32];
-  const int t = BLK ? threadIdx.x : threadIdx.x & (T - 1);
-  const int64_t row = BLK ? blockIdx.x
-                          : static_cast<int64_t>(blockIdx.x) * (blockDim.x / T) + threadIdx.x / T;
-  const bool live = BLK || row < rows;   // every lane stays for the shuffles
-  const int64_t base = row * d;
-  float h[C][V];
-  Raw<X, V> rx[C];
+  const int lane = threadIdx.x & (LANES - 1), part = threadIdx.x / LANES;
+  const int group = part / wide, w = part - group * wide;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / (LANES * wide)) + group;
+  const bool live = row < rows;   // all lanes and warps stay for shuffles and barriers
+  constexpr int kHop = LANES * V;
+  const int col0 = w * (H * kHop) + lane * V;
+  const int64_t base = row * d + col0;
+  float h[H][V];
+  Raw<X, V> rx[H];
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int col = (c * T + t) * V;
-    if (live && col < d) rx[c].load(x, base + col);
-  }
-  if (add) {
-    if (add_f32) {
-      Raw<F32, V> ra[C];
+  for (int c = 0; c < H; ++c)
+    if (live && col0 + c * kHop < d) rx[c].load(x, base + c * kHop);
+  const auto widen_sum = [&](auto& ra) {
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int col = (c * T + t) * V;
-        if (live && col < d) ra[c].load(add, base + col);
-      }
+    for (int c = 0; c < H; ++c)
+      if (live && col0 + c * kHop < d) ra[c].load(add, base + c * kHop);
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        float f[V];
-        rx[c].get(h[c]);
-        ra[c].get(f);
+    for (int c = 0; c < H; ++c) {
+      float f[V];
+      rx[c].get(h[c]);
+      ra[c].get(f);
 #pragma unroll
-        for (int v = 0; v < V; ++v) h[c][v] = rounded<X>(h[c][v] + f[v]);
-      }
-    } else {
-      Raw<BF16, V> ra[C];
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int col = (c * T + t) * V;
-        if (live && col < d) ra[c].load(add, base + col);
-      }
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        float f[V];
-        rx[c].get(h[c]);
-        ra[c].get(f);
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[c][v] = rounded<X>(h[c][v] + f[v]);
-      }
+      for (int v = 0; v < V; ++v) h[c][v] = rounded<X>(h[c][v] + f[v]);
+      if (live && col0 + c * kHop < d) Out<X, V>::store(sum, base + c * kHop, h[c]);
     }
+  };
+  if (!add) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int col = (c * T + t) * V;
-      if (live && col < d) Out<X, V>::store(sum, base + col, h[c]);
-    }
+    for (int c = 0; c < H; ++c) rx[c].get(h[c]);
+  } else if (add_f32) {
+    Raw<F32, V> ra[H];
+    widen_sum(ra);
   } else {
-#pragma unroll
-    for (int c = 0; c < C; ++c) rx[c].get(h[c]);
+    Raw<BF16, V> ra[H];
+    widen_sum(ra);
   }
   float s = 0.f;
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const bool in = live && (c * T + t) * V < d;
+  for (int c = 0; c < H; ++c) {
+    const bool in = live && col0 + c * kHop < d;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (!in) h[c][v] = 0.f;
       s += h[c][v];
     }
   }
-  const float mean = row_sum<BLK>(s, T, red[0]) / static_cast<float>(d);
+  const float mean = row_sum<LANES>(s, wide, group, w, &red[0][group * wide]) / static_cast<float>(d);
   float q = 0.f;
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const bool in = live && (c * T + t) * V < d;
+  for (int c = 0; c < H; ++c) {
+    const bool in = live && col0 + c * kHop < d;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       h[c][v] -= mean;
       if (in) q = fmaf(h[c][v], h[c][v], q);
     }
   }
-  const float rstd = 1.f / sqrtf(row_sum<BLK>(q, T, red[1]) / static_cast<float>(d) + eps);
-  if (live && t == 0) {
+  const float rstd = 1.f / sqrtf(row_sum<LANES>(q, wide, group, w, &red[1][group * wide]) /
+                                     static_cast<float>(d) + eps);
+  if (live && w == 0 && lane == 0) {
     if (mean_out) mean_out[row] = mean;
     if (rstd_out) rstd_out[row] = rstd;
   }
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int col = (c * T + t) * V;
+  for (int c = 0; c < H; ++c) {
+    const int col = col0 + c * kHop;
     if (!live || col >= d) continue;
     float g[V], b[V];
     load_param<V>(gamma, col, g);
@@ -135,13 +125,15 @@ layernorm_forward_kernel(const void* x, const void* add, int add_f32,
       const float n = h[c][v] * rstd * g[v];
       h[c][v] = beta ? n + b[v] : n;
     }
-    Out<Y, V>::store(y, base + col, h[c]);
+    Out<Y, V>::store(y, base + c * kHop, h[c]);
   }
 }
 
+int round32(int x) { return (x + 31) / 32 * 32; }
+
 struct FwdLaunch {
   int64_t rows;
-  int d, T, add_f32;
+  int d, add_f32;
   const void *x, *add;
   const float *gamma, *beta;
   void *y, *sum;
@@ -150,195 +142,425 @@ struct FwdLaunch {
   cudaStream_t st;
 };
 
-template <typename X, typename Y, int V, int C, bool BLK>
+template <typename X, typename Y, int V, int H, int LANES = 32>
 cudaError_t run_fwd(const FwdLaunch& l) {
-  const int threads = BLK ? l.T : 256;
-  const int per = BLK ? 1 : 256 / l.T;
+  const int wide = (l.d + LANES * V * H - 1) / (LANES * V * H);
+  // Blocks of 256 threads, or of one row that is wider.
+  const int per = LANES * wide >= 256 ? 1 : 256 / (LANES * wide);
+  const int threads = round32(LANES * wide * per);
   const int64_t blocks = (l.rows + per - 1) / per;
-  layernorm_forward_kernel<X, Y, V, C, BLK><<<static_cast<unsigned>(blocks), threads, 0, l.st>>>(
-      l.x, l.add, l.add_f32, l.gamma, l.beta, l.y, l.sum, l.mean, l.rstd, l.rows, l.d, l.T, l.eps);
+  layernorm_forward_kernel<X, Y, V, H, LANES>
+      <<<static_cast<unsigned>(blocks), threads, 0, l.st>>>(
+      l.x, l.add, l.add_f32, l.gamma, l.beta, l.y, l.sum, l.mean, l.rstd, l.rows, l.d, wide, l.eps);
   return cudaGetLastError();
 }
 
-int round32(int x) { return (x + 31) / 32 * 32; }
-
 template <typename X, typename Y>
-cudaError_t pick_fwd(FwdLaunch l) {
+cudaError_t pick_fwd(const FwdLaunch& l) {
   const int d = l.d;
-  if (d % 8 == 0) {
-    const int n = d / 8;   // 8-element chunks of a row
-    const bool few = l.rows <= 4 * sm_count();
-    if (n <= 8) { l.T = 8; return run_fwd<X, Y, 8, 1, false>(l); }
-    if (n <= 32) { l.T = 32; return run_fwd<X, Y, 8, 1, false>(l); }
-    if (few && n <= kMaxNormThreads) { l.T = round32(n); return run_fwd<X, Y, 8, 1, true>(l); }
-    if (n <= 64) { l.T = 32; return run_fwd<X, Y, 8, 2, false>(l); }
-    if (n <= 128) { l.T = 32; return run_fwd<X, Y, 8, 4, false>(l); }
-    if (n <= 256) { l.T = 32; return run_fwd<X, Y, 8, 8, false>(l); }
-    l.T = round32((n + 3) / 4);
-    return run_fwd<X, Y, 8, 4, true>(l);
+  if (d % 4 == 0) {
+    const int pieces = (d + 127) / 128;   // of a warp's access
+    if (d <= 64) return run_fwd<X, Y, 4, 2, 8>(l);
+    // Few rows: more warps for each, for latency. Else a warp for up to 512 columns (16384 fp32
+    // rows of 1600: 39 us, with 1024 columns 45), or 1024 where that is too many warps.
+    if (pieces <= 1 || (l.rows <= 4 * sm_count() && pieces <= 16)) return run_fwd<X, Y, 4, 1>(l);
+    if (pieces <= 2) return run_fwd<X, Y, 4, 2>(l);
+    if (pieces <= 32) return run_fwd<X, Y, 4, 4>(l);
+    return run_fwd<X, Y, 4, 8>(l);
   }
-  if (d <= 64) { l.T = 32; return run_fwd<X, Y, 1, 2, false>(l); }
-  if (d <= 256) { l.T = 32; return run_fwd<X, Y, 1, 8, false>(l); }
-  if (d <= 8 * kMaxNormThreads) { l.T = round32((d + 7) / 8); return run_fwd<X, Y, 1, 8, true>(l); }
-  l.T = round32((d + 31) / 32);
-  return run_fwd<X, Y, 1, 32, true>(l);
+  if (d <= 32) return run_fwd<X, Y, 1, 4, 8>(l);
+  if (d <= 128) return run_fwd<X, Y, 1, 4>(l);
+  if (d <= 16 * 32 * 8) return run_fwd<X, Y, 1, 8>(l);
+  if (d <= 16 * 32 * 16) return run_fwd<X, Y, 1, 16>(l);
+  return run_fwd<X, Y, 1, 32>(l);
 }
 
 // ------------------------------------------------------------------ backward
-// Groups of T threads (T <= 32: 256/T groups of a block, each with its own rows; else
-// the block is one group); group g of the grid takes the rows g, g + groups, ...
-template <typename X, typename G, typename O, int V, int C, bool BLK>
-__global__ void __launch_bounds__(BLK ? kMaxNormThreads : 256)
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <typename E> constexpr int kSize = sizeof(typename E::T);
+
+// Four elements from shared memory as pairs.
+struct Four {
+  Pair a, b;
+};
+template <bool F32_>
+__device__ __forceinline__ Four lds_four(uint32_t addr) {
+  Four f;
+  if (F32_) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    f.a = Pair(v.x, v.y), f.b = Pair(v.z, v.w);
+  } else {
+    uint32_t x, y;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(addr) : "memory");
+    f.a = Pair(bf16_lo(x), bf16_hi(x)), f.b = Pair(bf16_lo(y), bf16_hi(y));
+  }
+  return f;
+}
+
+template <typename O>
+__device__ __forceinline__ void store_four(void* base, int64_t i, Pair a, Pair b) {
+  const float2 x = a.get(), y = b.get();
+  if (kSize<O> == 4)
+    *reinterpret_cast<float4*>(static_cast<float*>(base) + i) = make_float4(x.x, x.y, y.x, y.y);
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + i) =
+        make_uint2(pack_bf16(x.x, x.y), pack_bf16(y.x, y.y));
+}
+
+// (-1/d) sums over the T threads of a row (or of two rows, R = 2) of s1 and s2, T <= 32 a power
+// of two (lanes of a warp) or a multiple of 32 (warps; `red` is then the half of the
+// group's array that this step uses: the halves alternate, so one barrier is enough).
+template <int R, bool WARPS>
+__device__ __forceinline__ void row_sums(float (&s1)[R], float (&s2)[R], int T, int group, int w,
+                                         float4* red, float ninv_d) {
+  if constexpr (WARPS) {
+    // The lanes' upper half goes on with s2; with two rows, the upper quarters with the second.
+    const bool up = threadIdx.x & 16, second = threadIdx.x & 8;
+    float v[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      v[r] = (up ? s2[r] : s1[r]) + __shfl_xor_sync(0xffffffffu, up ? s1[r] : s2[r], 16);
+    float q;
+    if constexpr (R == 2)
+      q = (second ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, second ? v[0] : v[1], 8);
+    else
+      q = v[0] + __shfl_xor_sync(0xffffffffu, v[0], 8);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+    if ((threadIdx.x & 7) == 0) reinterpret_cast<float*>(red + w)[(second ? 2 : 0) + up] = q;
+    group_barrier(group, T);
+    const int warps = T >> 5;
+    float4 f = red[0];
+#pragma unroll 4
+    for (int i = 1; i < warps; ++i) {
+      const float4 g = red[i];
+      f.x += g.x, f.y += g.y, f.z += g.z, f.w += g.w;
+    }
+    s1[0] = f.x * ninv_d, s2[0] = f.y * ninv_d;
+    if constexpr (R == 2) s1[1] = f.z * ninv_d, s2[1] = f.w * ninv_d;
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      for (int o = T >> 1; o > 0; o >>= 1) {
+        s1[r] += __shfl_xor_sync(0xffffffffu, s1[r], o);
+        s2[r] += __shfl_xor_sync(0xffffffffu, s2[r], o);
+      }
+      s1[r] *= ninv_d, s2[r] *= ninv_d;
+    }
+  }
+}
+
+// A block's partial column sums, added over its groups in order by way of sh[group][2][d], into
+// its row of `part`. Thread values are put in place by `put(destination of [2][d])`.
+template <typename Put>
+__device__ __forceinline__ void store_part(float* part, float* sh, int d, int group, int per,
+                                           const Put& put) {
+  float* pg = part + static_cast<int64_t>(blockIdx.x) * 2 * d;
+  put(per == 1 ? pg : sh + group * 2 * d);
+  if (per == 1) return;
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * d; i += blockDim.x) {
+    float s = 0.f;
+    for (int g = 0; g < per; ++g) s += sh[g * 2 * d + i];
+    pg[i] = s;
+  }
+}
+
+// Rows of 16-byte multiples (d a multiple of 8). A block holds `per` groups of T threads, group
+// g of the grid takes R rows at a time (two of up to 4096 columns: the reduction, the
+// barrier and the addresses, most of the instructions, come once for both). A warp (or, T <
+// 32, a group) owns spans of 8 columns a lane, each lane the four at 4 l and the four half
+// a span further, so that its accesses to fp32 and to bf16 arrays are both contiguous over
+// the lanes. It copies its spans of the next rows into shared memory ahead of time, 16
+// bytes a lane and contiguous (16 of every 32 bytes at a time took 71 us where this took 48,
+// 16384 fp32 rows of 1024), so memory stays busy across the reduction and barrier.
+template <typename X, typename G, typename O, int C, bool WARPS>
+__global__ void __launch_bounds__(kMaxNormThreads, 1)
 layernorm_backward_kernel(const void* gy, const void* x, const float* __restrict__ mean,
                           const float* __restrict__ rstd, const float* __restrict__ gamma,
                           const void* gsum, int gsum_f32, void* gx, float* part, int64_t rows,
-                          int d, int T) {
-  extern __shared__ float sh[];   // !BLK: column sums of the block's groups
-  __shared__ float red[2][2][kMaxNormThreads / 32];
-  const int t = BLK ? threadIdx.x : threadIdx.x & (T - 1);
-  const int per = BLK ? 1 : blockDim.x / T;
-  const int group = BLK ? 0 : threadIdx.x / T;
-  const float inv_d = 1.f / static_cast<float>(d);
-  float ag[C][V], ab[C][V];
+                          int d, int T, int per, int stages) {
+  extern __shared__ __align__(16) float sh[];   // the ring; at the end the groups' column sums
+  __shared__ float4 red[2][kMaxNormThreads / 32];
+  constexpr int R = C == 1 ? 2 : 1;
+  constexpr int kX = kSize<X>, kG = kSize<G>, kO = kSize<O>;
+  const int group = threadIdx.x / T;
+  const int t = threadIdx.x - group * T;
+  const int lanes = WARPS ? 32 : T;                    // of a span
+  const int l = t & (lanes - 1);
+  const int half = lanes * 4;                          // columns
+  const float ninv_d = -1.f / static_cast<float>(d);
+  const int ks = gsum ? (gsum_f32 ? 4 : 2) : 0;
+  const int span = lanes * 8 * (kX + kG + ks);         // bytes of one span of all arrays
+  const int at_g = lanes * 8 * kX, at_s = lanes * 8 * (kX + kG);
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(sh)) +
+                        static_cast<uint32_t>(threadIdx.x / lanes) * (stages * R * C * span);
+  const uint32_t ring_end = ring + stages * R * C * span;
+  const uint32_t nrows = static_cast<uint32_t>(rows), stride = gridDim.x * per * R;
+  const int first_col = (t / lanes) * 2 * half;        // of this warp's span, access 0
+  const int hop = T * 8;                               // columns from one access to the next
+  const uint32_t row_step = stride * d;                // elements
+
+  // Cursors of the copies (16 bytes a lane, two for fp32) and of the results.
+  uint32_t frow = (blockIdx.x * per + group) * R;      // the next row to copy
+  const int64_t start = static_cast<int64_t>(frow) * d + first_col;
+  const int lane16 = l * 16, wide = lanes * 16;        // bytes
+  const char* px = static_cast<const char*>(x) + start * kX + lane16;
+  const char* pg = static_cast<const char*>(gy) + start * kG + lane16;
+  const char* ps = static_cast<const char*>(gsum) + start * ks + lane16;
+  char* po = static_cast<char*>(gx) + (start + 4 * l) * kO;
+  const auto copy = [&](uint32_t dst, const char* p, int left, int size) {
+    if (left > 0) copy_async16(dst, p);
+    if (size == 4 && left > wide) copy_async16(dst + wide, p + wide);
+  };
+  uint32_t fslot = ring + lane16;
+  const auto prefetch = [&]() {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (frow + r < nrows) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const int left = d - first_col - c * hop;    // columns
+          const uint32_t dst = fslot + (r * C + c) * span;
+          copy(dst, px + (c * hop + r * d) * kX, left * kX - lane16, kX);
+          copy(dst + at_g, pg + (c * hop + r * d) * kG, left * kG - lane16, kG);
+          if (ks == 4) copy(dst + at_s, ps + (c * hop + r * d) * 4, left * 4 - lane16, 4);
+          else if (ks == 2) copy(dst + at_s, ps + (c * hop + r * d) * 2, left * 2 - lane16, 2);
+        }
+      }
+    }
+    copy_commit();                                     // empty groups keep the count
+    px += static_cast<int64_t>(row_step) * kX;
+    pg += static_cast<int64_t>(row_step) * kG;
+    ps += static_cast<int64_t>(row_step) * ks;
+    frow += stride;
+    fslot += R * C * span;
+    if (fslot >= ring_end) fslot -= stages * R * C * span;
+  };
+
+  // [c][h]: columns first_col + c hop + h half + 4 l.
+  Pair ag[C][2][2], ab[C][2][2], gm[C][2][2];
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int v = 0; v < V; ++v) ag[c][v] = ab[c][v] = 0.f;
+    for (int h = 0; h < 2; ++h) {
+      const int col = first_col + c * hop + h * half + 4 * l;
+      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (col < d) f = __ldg(reinterpret_cast<const float4*>(gamma + col));
+      gm[c][h][0] = Pair(f.x, f.y), gm[c][h][1] = Pair(f.z, f.w);
+      ag[c][h][0] = ag[c][h][1] = ab[c][h][0] = ab[c][h][1] = Pair(0.f);
+    }
+  uint32_t row = frow;
+  const float* pm = mean + row;
+  const float* pr = rstd + row;
+  for (int k = 0; k < stages - 1; ++k) prefetch();
+  float mu[R] = {}, rstd_row[R] = {};
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (row + r < nrows) mu[r] = __ldg(pm + r), rstd_row[r] = __ldg(pr + r);
+  float4* my_red = &red[0][group * (T >> 5)];
+  uint32_t slot = ring;
+  // Block-uniform trip count: every thread takes part in the reductions.
+  for (uint32_t r0 = blockIdx.x * per * R; r0 < nrows; r0 += stride, row += stride) {
+    __syncwarp();                                      // the slot has been read by every lane
+    prefetch();
+    pm += stride, pr += stride;
+    float mu_next[R] = {}, rs_next[R] = {};
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (row + stride + r < nrows) mu_next[r] = __ldg(pm + r), rs_next[r] = __ldg(pr + r);
+    if (stages == 3) copy_wait<2>();
+    else if (stages == 2) copy_wait<1>();
+    else copy_wait<0>();
+    __syncwarp();
+    Pair xh[R][C][2][2], tt[R][C][2][2];
+    float s1[R], s2[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      Pair p1(0.f), p2(0.f);
+      if (row + r < nrows) {
+        // xhat = (x - mean) rstd as one fused operation.
+        const Pair rs(rstd_row[r]), off(-mu[r] * rstd_row[r]);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (first_col + c * hop + h * half + 4 * l >= d) continue;
+            const uint32_t at = slot + (r * C + c) * span;
+            const Four fx = lds_four<kX == 4>(at + (h * half + 4 * l) * kX);
+            const Four fg = lds_four<kG == 4>(at + at_g + (h * half + 4 * l) * kG);
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              const Pair g = v ? fg.b : fg.a;
+              const Pair q = fma(v ? fx.b : fx.a, rs, off);
+              const Pair w = mul(g, gm[c][h][v]);
+              ag[c][h][v] = fma(g, q, ag[c][h][v]);
+              ab[c][h][v] = add(g, ab[c][h][v]);
+              p1 = add(w, p1);
+              p2 = fma(w, q, p2);
+              xh[r][c][h][v] = q;
+              tt[r][c][h][v] = w;
+            }
+          }
+      }
+      s1[r] = p1.lo() + p1.hi(), s2[r] = p2.lo() + p2.hi();
+    }
+    row_sums<R, WARPS>(s1, s2, T, group, t >> 5, my_red, ninv_d);
+    my_red = my_red >= red[1] ? my_red - kMaxNormThreads / 32 : my_red + kMaxNormThreads / 32;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (row + r >= nrows) continue;
+      const Pair rs(rstd_row[r]), m1(s1[r]), m2(s2[r]);
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (first_col + c * hop + h * half + 4 * l >= d) continue;
+          Pair o[2];
+#pragma unroll
+          for (int v = 0; v < 2; ++v) o[v] = add(fma(xh[r][c][h][v], m2, tt[r][c][h][v]), m1);
+          if (ks) {
+            const uint32_t as = slot + (r * C + c) * span + at_s + (h * half + 4 * l) * ks;
+            const Four f = ks == 4 ? lds_four<true>(as) : lds_four<false>(as);
+            o[0] = fma(o[0], rs, f.a), o[1] = fma(o[1], rs, f.b);
+          } else {
+            o[0] = mul(o[0], rs), o[1] = mul(o[1], rs);
+          }
+          store_four<O>(po, r * d + c * hop + h * half, o[0], o[1]);
+        }
+    }
+    po += static_cast<int64_t>(row_step) * kO;
+#pragma unroll
+    for (int r = 0; r < R; ++r) mu[r] = mu_next[r], rstd_row[r] = rs_next[r];
+    slot += R * C * span;
+    if (slot == ring_end) slot = ring;
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!part) return;
+  copy_wait<0>();
+  __syncthreads();                                     // the ring is free
+  store_part(part, sh, d, group, per, [&](float* to) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int col = first_col + c * hop + h * half + 4 * l;
+        if (col >= d) continue;
+        store_four<F32>(to, col, ag[c][h][0], ag[c][h][1]);
+        store_four<F32>(to, d + col, ab[c][h][0], ab[c][h][1]);
+      }
+  });
+}
+
+// Rows of any other length: one element at a time (a warp's accesses are contiguous).
+template <typename X, typename G, typename O, int C, bool WARPS>
+__global__ void __launch_bounds__(kMaxNormThreads)
+layernorm_backward_odd_kernel(const void* gy, const void* x, const float* __restrict__ mean,
+                              const float* __restrict__ rstd, const float* __restrict__ gamma,
+                              const void* gsum, int gsum_f32, void* gx, float* part, int64_t rows,
+                              int d, int T, int per) {
+  extern __shared__ float sh[];   // the groups' column sums
+  __shared__ float4 red[2][kMaxNormThreads / 32];
+  const int group = threadIdx.x / T;
+  const int t = threadIdx.x - group * T;
+  const float inv_d = 1.f / static_cast<float>(d);
+  float ag[C], ab[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) ag[c] = ab[c] = 0.f;
   int flip = 0;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * per;
-  // Block-uniform trip count: every thread takes part in the reductions.
   for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * per; r0 < rows; r0 += stride, flip ^= 1) {
     const int64_t row = r0 + group;
     const bool live = row < rows;
     const int64_t base = row * d;
-    Raw<X, V> rx[C];
-    Raw<G, V> rg[C];
+    Raw<X, 1> rx[C];
+    Raw<G, 1> rg[C];
+    float s[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int col = (c * T + t) * V;
+      const int col = c * T + t;
       if (live && col < d) {
         rx[c].load(x, base + col);
         rg[c].load(gy, base + col);
+        s[c] = gsum ? (gsum_f32 ? load_elem(static_cast<const float*>(gsum), base + col)
+                                : load_elem(static_cast<const uint16_t*>(gsum), base + col))
+                    : 0.f;
       }
     }
     const float mu = live ? mean[row] : 0.f, rs = live ? rstd[row] : 0.f;
     float s1 = 0.f, s2 = 0.f;
+    float xh[C], tt[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int col = (c * T + t) * V;
+      const int col = c * T + t;
       if (live && col < d) {
-        float xv[V], gv[V], gm[V];
-        rx[c].get(xv);
-        rg[c].get(gv);
-        load_param<V>(gamma, col, gm);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float xh = (xv[v] - mu) * rs;
-          const float tt = gv[v] * gm[v];
-          s1 += tt;
-          s2 = fmaf(tt, xh, s2);
-          ag[c][v] = fmaf(gv[v], xh, ag[c][v]);
-          ab[c][v] += gv[v];
-        }
+        float xv, gv;
+        rx[c].get(&xv);
+        rg[c].get(&gv);
+        xh[c] = (xv - mu) * rs;
+        tt[c] = gv * __ldg(gamma + col);
+        s1 += tt[c];
+        s2 = fmaf(tt[c], xh[c], s2);
+        ag[c] = fmaf(gv, xh[c], ag[c]);
+        ab[c] += gv;
       }
     }
-    const int w = BLK ? 32 : T;
-    for (int o = w >> 1; o > 0; o >>= 1) {
-      s1 += __shfl_xor_sync(0xffffffffu, s1, o);
-      s2 += __shfl_xor_sync(0xffffffffu, s2, o);
-    }
-    if (BLK) {
-      // The two halves of `red` alternate, so one barrier per row is enough.
-      if ((threadIdx.x & 31) == 0) {
-        red[flip][0][threadIdx.x >> 5] = s1;
-        red[flip][1][threadIdx.x >> 5] = s2;
-      }
-      __syncthreads();
-      s1 = s2 = 0.f;
-      for (int i = 0; i < (T >> 5); ++i) {
-        s1 += red[flip][0][i];
-        s2 += red[flip][1][i];
-      }
-    }
-    s1 *= inv_d;
-    s2 *= inv_d;
+    float a1[1] = {s1}, a2[1] = {s2};
+    row_sums<1, WARPS>(a1, a2, T, group, t >> 5, &red[flip][group * (T >> 5)], -inv_d);
+    s1 = -a1[0], s2 = -a2[0];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int col = (c * T + t) * V;
+      const int col = c * T + t;
       if (!live || col >= d) continue;
-      float xv[V], gv[V], gm[V], o[V];
-      rx[c].get(xv);
-      rg[c].get(gv);
-      load_param<V>(gamma, col, gm);
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        o[v] = rs * (gv[v] * gm[v] - s1 - (xv[v] - mu) * rs * s2);
-      if (gsum) {
-        float f[V];
-        if (gsum_f32) {
-          Raw<F32, V> q;
-          q.load(gsum, base + col);
-          q.get(f);
-        } else {
-          Raw<BF16, V> q;
-          q.load(gsum, base + col);
-          q.get(f);
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) o[v] += f[v];
-      }
-      Out<O, V>::store(gx, base + col, o);
+      const float o = rs * (tt[c] - s1 - xh[c] * s2) + s[c];
+      Out<O, 1>::store(gx, base + col, &o);
     }
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!part) return;
-  float* pg = part + static_cast<int64_t>(blockIdx.x) * 2 * d;
-  if (BLK) {
+  store_part(part, sh, d, group, per, [&](float* to) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int col = (c * T + t) * V;
+      const int col = c * T + t;
       if (col >= d) continue;
-      Out<F32, V>::store(pg, col, ag[c]);
-      Out<F32, V>::store(pg + d, col, ab[c]);
+      to[col] = ag[c];
+      to[d + col] = ab[c];
     }
-  } else {
-    // Groups in order: sh[group][2][d]; then each column is added over the groups.
-    float* mine = sh + group * 2 * d;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int col = (c * T + t) * V;
-      if (col >= d) continue;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        mine[col + v] = ag[c][v];
-        mine[d + col + v] = ab[c][v];
-      }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * d; i += blockDim.x) {
-      float s = 0.f;
-      for (int g = 0; g < per; ++g) s += sh[g * 2 * d + i];
-      pg[i] = s;
-    }
-  }
+  });
 }
 
 // grad_gamma / grad_beta = column sums of the partial rows [blocks][2 d]: 32 columns a
-// block, 8 rows at a time per column, the 8 strands added in order.
-__global__ void __launch_bounds__(256) layernorm_columns_kernel(const float* __restrict__ part,
-                                                                int blocks, int d, float* gg,
-                                                                float* gb) {
-  __shared__ float sh[8][33];
+// block, 32 strands of rows per column, added in order.
+constexpr int kStrands = 32;
+__global__ void __launch_bounds__(32 * kStrands) layernorm_columns_kernel(const float* part,
+                                                                         int blocks, int d,
+                                                                         float* gg, float* gb) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ float sh[kStrands][33];
   const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + c;
   float s = 0.f;
-  if (col < 2 * d)
-    for (int r = k; r < blocks; r += 8) s += part[static_cast<int64_t>(r) * 2 * d + col];
+  if (col < 2 * d) {
+#pragma unroll 4
+    for (int r = k; r < blocks; r += kStrands) s += part[static_cast<int64_t>(r) * 2 * d + col];
+  }
   sh[k][c] = s;
   __syncthreads();
   if (k == 0 && col < 2 * d) {
     float a = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a += sh[i][c];
+    for (int i = 0; i < kStrands; ++i) a += sh[i][c];
     if (col < d) {
       if (gg) gg[col] = a;
     } else if (gb) {
@@ -347,9 +569,38 @@ __global__ void __launch_bounds__(256) layernorm_columns_kernel(const float* __r
   }
 }
 
+// How the backward's rows are shared out: groups of T threads with C accesses of 8 (or, odd
+// widths, 1) elements each and R rows at a time, `per` groups a block of at most 512
+// threads, and at most one block for each of the 148 SMs of a B200 (the workspace's size
+// depends on the number of blocks, so on the sizes alone).
+struct NormGroups {
+  int T, C, R, per, blocks;
+};
+
+NormGroups norm_groups(int64_t rows, int d) {
+  NormGroups n;
+  n.R = 1;
+  if (d % 8 == 0) {
+    const int chunks = d / 8;
+    n.C = chunks <= kMaxNormThreads ? 1 : (chunks <= 2 * kMaxNormThreads ? 2 : 4);
+    n.T = chunks <= 8 ? 8 : round32((chunks + n.C - 1) / n.C);
+    if (n.C == 1) n.R = 2;
+  } else {
+    n.C = d <= 64 ? 2 : (d <= 8 * kMaxNormThreads ? 8 : (d <= 16 * kMaxNormThreads ? 16 : 32));
+    n.T = round32((d + n.C - 1) / n.C);
+  }
+  n.per = kMaxNormThreads / n.T;
+  if (n.T > 32 && n.per > 8) n.per = 8;                  // barriers: one for each group
+  while (n.per > 1 && (rows + n.per * n.R - 1) / (n.per * n.R) < 148) --n.per;   // every SM first
+  while (n.T * n.per % 32) ++n.per;                      // whole warps
+  const int64_t want = (rows + n.per * n.R - 1) / (n.per * n.R);
+  n.blocks = static_cast<int>(want < 148 ? (want > 0 ? want : 1) : 148);
+  return n;
+}
+
 struct BwdLaunch {
   int64_t rows;
-  int d, T, gsum_f32, blocks;
+  int d, gsum_f32, blocks;
   const void *gy, *x, *gsum;
   const float *mean, *rstd, *gamma;
   void* gx;
@@ -357,30 +608,47 @@ struct BwdLaunch {
   cudaStream_t st;
 };
 
-template <typename X, typename G, typename O, int V, int C, bool BLK>
-cudaError_t run_bwd(const BwdLaunch& l) {
-  const int threads = BLK ? l.T : 256;
-  const size_t smem = BLK ? 0 : static_cast<size_t>(256 / l.T) * 2 * l.d * sizeof(float);
-  layernorm_backward_kernel<X, G, O, V, C, BLK><<<l.blocks, threads, smem, l.st>>>(
-      l.gy, l.x, l.mean, l.rstd, l.gamma, l.gsum, l.gsum_f32, l.gx, l.part, l.rows, l.d, l.T);
+constexpr size_t kRingBytes = 220 * 1024;                // one block an SM
+
+template <typename X, typename G, typename O, int C, bool WARPS>
+cudaError_t run_bwd(const BwdLaunch& l, const NormGroups& n) {
+  const int threads = n.T * n.per;
+  const size_t sums = n.per > 1 ? static_cast<size_t>(n.per) * 2 * l.d * sizeof(float) : 0;
+  const size_t row = static_cast<size_t>(C == 1 ? 2 : C) * threads * 8 *
+                     (kSize<X> + kSize<G> + (l.gsum ? (l.gsum_f32 ? 4 : 2) : 0));
+  int stages = 1;                                        // 1: rows of 16384 in fp32, not ahead
+  while (stages < 3 && (stages + 1) * row <= kRingBytes) ++stages;
+  const size_t smem = stages * row > sums ? stages * row : sums;
+  auto* kernel = layernorm_backward_kernel<X, G, O, C, WARPS>;
+  cudaError_t e = set_max_smem(reinterpret_cast<const void*>(kernel), smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<n.blocks, threads, smem, l.st>>>(l.gy, l.x, l.mean, l.rstd, l.gamma, l.gsum, l.gsum_f32,
+                                            l.gx, l.part, l.rows, l.d, n.T, n.per, stages);
+  return cudaGetLastError();
+}
+
+template <typename X, typename G, typename O, int C, bool WARPS>
+cudaError_t run_bwd_odd(const BwdLaunch& l, const NormGroups& n) {
+  const size_t smem = n.per > 1 ? static_cast<size_t>(n.per) * 2 * l.d * sizeof(float) : 0;
+  layernorm_backward_odd_kernel<X, G, O, C, WARPS><<<n.blocks, n.T * n.per, smem, l.st>>>(
+      l.gy, l.x, l.mean, l.rstd, l.gamma, l.gsum, l.gsum_f32, l.gx, l.part, l.rows, l.d, n.T,
+      n.per);
   return cudaGetLastError();
 }
 
 template <typename X, typename G, typename O>
-cudaError_t pick_bwd(BwdLaunch l) {
-  const int d = l.d;
-  if (d % 8 == 0) {
-    const int n = d / 8;
-    if (n <= 8) { l.T = 8; return run_bwd<X, G, O, 8, 1, false>(l); }
-    if (n <= 32) { l.T = 32; return run_bwd<X, G, O, 8, 1, false>(l); }
-    if (n <= kMaxNormThreads) { l.T = round32(n); return run_bwd<X, G, O, 8, 1, true>(l); }
-    l.T = round32((n + 3) / 4);
-    return run_bwd<X, G, O, 8, 4, true>(l);
+cudaError_t pick_bwd(const BwdLaunch& l) {
+  const NormGroups n = norm_groups(l.rows, l.d);
+  if (l.d % 8 == 0) {
+    if (n.T <= 32) return run_bwd<X, G, O, 1, false>(l, n);
+    if (n.C == 1) return run_bwd<X, G, O, 1, true>(l, n);
+    if (n.C == 2) return run_bwd<X, G, O, 2, true>(l, n);
+    return run_bwd<X, G, O, 4, true>(l, n);
   }
-  if (d <= 64) { l.T = 32; return run_bwd<X, G, O, 1, 2, false>(l); }
-  if (d <= 8 * kMaxNormThreads) { l.T = round32((d + 7) / 8); return run_bwd<X, G, O, 1, 8, true>(l); }
-  l.T = round32((d + 31) / 32);
-  return run_bwd<X, G, O, 1, 32, true>(l);
+  if (n.C == 2) return run_bwd_odd<X, G, O, 2, false>(l, n);
+  if (n.C == 8) return run_bwd_odd<X, G, O, 8, true>(l, n);
+  if (n.C == 16) return run_bwd_odd<X, G, O, 16, true>(l, n);
+  return run_bwd_odd<X, G, O, 32, true>(l, n);
 }
 
 }  // namespace
@@ -388,28 +656,20 @@ cudaError_t pick_bwd(BwdLaunch l) {
 cudaError_t launch_layernorm_forward(const NormArgs& a, const void* x, const void* add,
                                      const float* gamma, const float* beta, void* y, void* sum,
                                      float* mean, float* rstd, cudaStream_t st) {
-  FwdLaunch l{a.rows, a.d, 0, a.add_dtype == 0, x, add, gamma, beta, y, sum, mean, rstd, a.eps, st};
+  FwdLaunch l{a.rows, a.d, a.add_dtype == 0, x, add, gamma, beta, y, sum, mean, rstd, a.eps, st};
   const bool xf = a.x_dtype == 0, yf = a.y_dtype == 0;
   if (xf) return yf ? pick_fwd<F32, F32>(l) : pick_fwd<F32, BF16>(l);
   return yf ? pick_fwd<BF16, F32>(l) : pick_fwd<BF16, BF16>(l);
 }
 
-// Blocks of the backward: a few per SM (148 on a B200), fewer when there are fewer
-// groups of rows. The workspace is sized by it, so it depends on the sizes alone.
-int norm_backward_blocks(int64_t rows, int d) {
-  const bool vec = d % 8 == 0;
-  const int per = vec ? (d <= 64 ? 32 : (d <= 256 ? 8 : 1)) : (d <= 64 ? 8 : 1);
-  const int64_t want = (rows + per - 1) / per;
-  const int64_t most = 148 * 4;
-  return static_cast<int>(want < most ? (want > 0 ? want : 1) : most);
-}
+int norm_backward_blocks(int64_t rows, int d) { return norm_groups(rows, d).blocks; }
 
 cudaError_t launch_layernorm_backward(const NormArgs& a, const void* grad_y, const void* x,
                                       const float* mean, const float* rstd, const float* gamma,
                                       const void* grad_sum, void* grad_x, float* grad_gamma,
                                       float* grad_beta, float* part, cudaStream_t st) {
   const bool sums = grad_gamma || grad_beta;
-  BwdLaunch l{a.rows, a.d, 0, a.add_dtype == 0, norm_backward_blocks(a.rows, a.d), grad_y, x,
+  BwdLaunch l{a.rows, a.d, a.add_dtype == 0, norm_backward_blocks(a.rows, a.d), grad_y, x,
               grad_sum, mean, rstd, gamma, grad_x, sums ? part : nullptr, st};
   const bool xf = a.x_dtype == 0, gf = a.y_dtype == 0, of = a.grad_dtype == 0;
   cudaError_t e;
@@ -421,9 +681,18 @@ cudaError_t launch_layernorm_backward(const NormArgs& a, const void* grad_y, con
     else e = of ? pick_bwd<BF16, BF16, F32>(l) : pick_bwd<BF16, BF16, BF16>(l);
   }
   if (e != cudaSuccess || !sums) return e;
-  layernorm_columns_kernel<<<(2 * a.d + 31) / 32, 256, 0, st>>>(part, l.blocks, a.d, grad_gamma,
-                                                               grad_beta);
-  return cudaGetLastError();
+  // Scheduled while the last rows are written; waits on the device for their end.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((2 * a.d + 31) / 32);
+  cfg.blockDim = dim3(32 * kStrands);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, layernorm_columns_kernel, static_cast<const float*>(part),
+                            l.blocks, a.d, grad_gamma, grad_beta);
 }
 
 }  // namespace pkm
