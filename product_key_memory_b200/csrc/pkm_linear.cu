@@ -176,7 +176,7 @@ cudaError_t make_planes(const void* src, int dtype, uint16_t* dst, int64_t rows,
 // written as NP planes (NP = 0: not needed) and its column sums as one partial row per block
 // row (part NULL: not needed).
 constexpr int kPrepRows = 64;
-constexpr int kDeep = 4;           // rows in flight per thread
+constexpr int kDeep = 2;           // rows in flight per thread
 
 template <typename E, int V, int NP>
 __global__ void __launch_bounds__(256) linear_slope_kernel(const void* gy, const void* pre,
@@ -306,16 +306,12 @@ LinearWork share_out(int64_t M, int64_t N, int64_t K, int products) {
   return best;
 }
 
-struct PlaneSet {
-  uint32_t a, b;
-  int products;
-};
-
-// The plane pairs of a product, p + q below the larger plane count, smallest first.
-PlaneSet plane_pairs(int a, int b) {
-  if (a == 3 && b == 3) return {0x001012u, 0x010210u, 6};   // (2,0) (1,1) (0,2) (1,0) (0,1) (0,0)
-  if (a == 2) return {0x01u, 0x00u, 2};                     // (1,0) (0,0)
-  return {0u, 0u, 1};
+// The products of a's and b's planes, p + q below the larger plane count, smallest first.
+LinearSteps plane_steps(int a, int b) {
+  // (planes of A, plane of B): {0} 2, {1, 0} 1, {2, 1} 0, {0} 0.
+  if (a == 3 && b == 3) return {0x1000'2012'2101'1200ull, 4, 6};
+  if (a == 2) return {0x2001, 1, 2};                                    // {1, 0} 0
+  return {0x1000, 1, 1};
 }
 
 // Number of planes of an operand of the layer's type; in place (0 bytes) for bf16 rows of
@@ -341,7 +337,7 @@ int slope_planes(const LinearArgs& a) {
 struct Layout {
   size_t x, W, d, part, bias, total;   // offsets; total = bytes
   LinearWork fwd, gx, gw;
-  PlaneSet fwd_p, gx_p, gw_p;
+  LinearSteps fwd_p, gx_p, gw_p;
 };
 
 Layout layout(const LinearArgs& a, bool backward) {
@@ -354,14 +350,14 @@ Layout layout(const LinearArgs& a, bool backward) {
   off += planes_bytes(a.dtype, a.N, a.K);
   l.part = off;
   if (!backward) {
-    l.fwd_p = plane_pairs(in, in);
+    l.fwd_p = plane_steps(in, in);
     l.fwd = share_out(a.M, a.N, a.K, l.fwd_p.products);
     off += part_bytes(l.fwd);
   } else {
     const int d = slope_planes(a);
     // grad_x in bf16: d's rounding to bf16 is no larger than grad_x's own, one plane will do.
-    l.gx_p = plane_pairs(d == 2 && a.out_dtype == PKM_BF16 ? 1 : (d ? d : 1), in);
-    l.gw_p = plane_pairs(d ? d : 1, in);
+    l.gx_p = plane_steps(d == 2 && a.out_dtype == PKM_BF16 ? 1 : (d ? d : 1), in);
+    l.gw_p = plane_steps(d ? d : 1, in);
     l.gx = share_out(a.M, a.K, a.N, l.gx_p.products);
     l.gw = share_out(a.N, a.K, a.M, l.gw_p.products);
     const size_t px = part_bytes(l.gx), pw = part_bytes(l.gw);
@@ -416,8 +412,7 @@ cudaError_t launch_linear_forward(const LinearArgs& a, const void* x, const void
     *launches += 2;
   }
   const uint32_t in = static_cast<uint32_t>(input_planes(a.dtype));
-  const LinearGemm g{kForward, x, W, ld, ld, static_cast<int>(a.M), a.N, a.K, in, in, l.fwd_p.a,
-                     l.fwd_p.b, l.fwd_p.products, l.fwd,
+  const LinearGemm g{kForward, x, W, ld, ld, static_cast<int>(a.M), a.N, a.K, in, in, l.fwd_p, l.fwd,
                      l.fwd.cut ? reinterpret_cast<float*>(ws + l.part) : nullptr, epi, status,
                      first != nullptr};
   return launch_linear_gemm(g, launches, st);
@@ -473,7 +468,7 @@ cudaError_t launch_linear_backward(const LinearArgs& a, const void* x, const voi
     const LinearEpilogue epi{grad_x, nullptr, nullptr, nullptr, a.out_dtype == PKM_F32, 0,
                              PKM_ACT_NONE};
     const LinearGemm g{kGradX, dop, W, ldn, ldk, static_cast<int>(a.M), a.K, a.N, dcount, in,
-                       l.gx_p.a, l.gx_p.b, l.gx_p.products, l.gx, l.gx.cut ? part : nullptr, epi,
+                       l.gx_p, l.gx, l.gx.cut ? part : nullptr, epi,
                        status, first != nullptr};
     e = launch_linear_gemm(g, launches, st);
     if (e != cudaSuccess) return e;
@@ -489,7 +484,7 @@ cudaError_t launch_linear_backward(const LinearArgs& a, const void* x, const voi
     }
     const LinearEpilogue epi{grad_W, nullptr, nullptr, nullptr, 1, 0, PKM_ACT_NONE};
     const LinearGemm g{kGradW, dop, x, ldn, ldk, a.N, a.K, static_cast<int>(a.M), dcount, in,
-                       l.gw_p.a, l.gw_p.b, l.gw_p.products, l.gw, l.gw.cut ? part : nullptr, epi,
+                       l.gw_p, l.gw, l.gw.cut ? part : nullptr, epi,
                        status, first != nullptr};
     e = launch_linear_gemm(g, launches, st);
   }

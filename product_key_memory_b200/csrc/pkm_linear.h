@@ -36,18 +36,23 @@ struct LinearWork {
   }
 };
 
+// The plane products of one K block: step i (16 bits from bit 16 i) multiplies `count` planes of
+// A (bits 12..15), nibbles 0.. in this order, with one plane of B (nibble 2).
+struct LinearSteps {
+  uint64_t packed;
+  int count, products;
+};
+
 // One product C[M][N] over K. A: K-major [a_count][M][lda] (forward, grad_x) or MN-major
 // [a_count][K][lda] (grad_W); B: K-major [b_count][N][ldb] (forward) or MN-major
-// [b_count][K][ldb]. The sum runs over `products` plane pairs, pair i being A's nibble i of
-// a_planes with B's nibble i of b_planes. Leading dimensions are multiples of 8.
+// [b_count][K][ldb]. Leading dimensions are multiples of 8.
 struct LinearGemm {
   LinearLayout layout;
   const void *a, *b;
   int64_t lda, ldb;
   int M, N, K;
   uint32_t a_count, b_count;
-  uint32_t a_planes, b_planes;
-  int products;
+  LinearSteps steps;
   LinearWork work;
   float* part;     // [2 pairs][256][256] fp32 when tiles are cut, else NULL
   LinearEpilogue epi;

@@ -9,7 +9,9 @@
 // No operand is transposed in memory; the MMA's instruction descriptor carries the
 // majorness. bf16 operands are one plane. An fp32 operand arrives as bf16 planes
 // hi, mid, lo whose sum is the value to 2^-24, and the products whose size is above 2^-24
-// are added in one fp32 accumulator, the K loop running over (K block, plane pair).
+// are added in one fp32 accumulator. A step of the K loop is one K block of one plane of B
+// and of up to AP planes of A, each multiplied with it: a B tile is loaded once for two
+// products.
 //
 // A tile is 256 x 256 outputs of a pair of CTAs that shares each MMA (cta_group::2): every
 // CTA loads half of A's rows and half of B's columns. What bounds the product is the
@@ -29,8 +31,8 @@
 // 2^-24 of it towards zero, so K / 16 cuts add up (1e-5 of the result at K = 8192). Where
 // the output is fp32 (PROMOTE) the accumulator is therefore taken out every kSegment K
 // blocks and added to fp32 registers, rounded to nearest; the epilogue warps do that while
-// the next segment is multiplied into the other half of TMEM. Plane pairs go smallest
-// first inside a segment, so the small ones are added to small sums.
+// the next segment is multiplied into the other half of TMEM. The steps of a K block go
+// smallest products first.
 //
 // Epilogue: with PROMOTE 8 warps (two per TMEM lane quadrant; their accumulators take the
 // registers), else up to 16, whose activations hide one another's latencies. A thread owns
@@ -52,14 +54,14 @@ constexpr int kRows = kLinearTileM / 2;  // of a tile per CTA
 constexpr int BN = kLinearTileN;
 constexpr int kCols = BN / 2;            // columns of B per CTA
 constexpr int kK = 64;                   // K per stage: one 128-byte swizzled row of bf16
-constexpr int kSegment = 8;              // K blocks between two takings (PROMOTE)
+constexpr int kSegment = 8;              // K blocks between two takings (PROMOTE); planes: 4
 constexpr uint32_t kABytes = kRows * kK * 2;
 constexpr uint32_t kMnBlock = 64 * kK * 2;   // 64 MN x 64 K of an MN-major operand
 
-template <bool PROMOTE> struct Tile {
+template <int AP, bool PROMOTE> struct Tile {
   static constexpr uint32_t kBBytes = kCols * kK * 2;
-  static constexpr uint32_t kStage = kABytes + kBBytes;
-  static constexpr int kStages = 163840 / kStage;            // 160 KiB of stages
+  static constexpr uint32_t kStage = AP * kABytes + kBBytes;
+  static constexpr int kStages = 163840 / kStage;            // up to 160 KiB of stages
   // Epilogue warps: each takes kWide columns of its quadrant's rows.
   static constexpr int kWide = PROMOTE ? BN / 2 : BN / 4;
   static constexpr int kEpi = 4 * (BN / kWide);
@@ -83,18 +85,11 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t addr) {
          ((1024ull >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// The steps of a product run over segments of `seg` K blocks, in each over the plane pairs,
-// in each over the K blocks.
-struct Step {
-  int kb = 0, pair = 0, from = 0;
-  __device__ __forceinline__ void advance(int kblocks, int seg, int products) {
-    if (++kb < min(from + seg, kblocks)) return;
-    kb = from;
-    if (++pair < products) return;
-    pair = 0;
-    kb = from = min(from + seg, kblocks);
-  }
-};
+// The steps of one K block (LinearSteps), packed into 16 bits each: A's planes in the order of
+// their products, B's plane, and the number of A's planes.
+__device__ __forceinline__ int step_planes(uint64_t steps, int i) {
+  return static_cast<int>(steps >> (16 * i)) & 0xffff;
+}
 
 // Tiles go in groups of kGroupM rows of tiles, down the group's rows first: the tiles in
 // flight at a time share their operands in both directions.
@@ -311,14 +306,14 @@ __device__ __forceinline__ void store_part(const CUtensorMap* tm_part, Outputs& 
   o.part_before = true;
 }
 
-template <bool A_MN, bool B_MN, bool PROMOTE>
-__global__ void __launch_bounds__(Tile<PROMOTE>::kThreads, 1) linear_tc_kernel(
+template <bool A_MN, bool B_MN, int AP, bool PROMOTE>
+__global__ void __launch_bounds__(Tile<AP, PROMOTE>::kThreads, 1) linear_tc_kernel(
     const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
     const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_pre,
-    const __grid_constant__ CUtensorMap tm_part, int M, int N, uint32_t a_planes,
-    uint32_t b_planes, int products, const LinearWork plan, int use_tma, const LinearEpilogue epi,
+    const __grid_constant__ CUtensorMap tm_part, int M, int N, const uint64_t steps,
+    const int nsteps, const LinearWork plan, int use_tma, const LinearEpilogue epi,
     int* status, int clear) {
-  using T = Tile<PROMOTE>;
+  using T = Tile<AP, PROMOTE>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = align1024(smem_raw);
   uint8_t* staging = stages + T::kStages * T::kStage;
@@ -336,7 +331,7 @@ __global__ void __launch_bounds__(Tile<PROMOTE>::kThreads, 1) linear_tc_kernel(
   const int nt = (N + BN - 1) / BN;
   const int pair = blockIdx.x >> 1;
   // Segments of a piece of k K blocks.
-  const auto segment = [](int k) { return PROMOTE ? kSegment : k; };
+  const auto segment = [](int k) { return PROMOTE ? (AP > 1 ? kSegment / 2 : kSegment) : k; };
   // The join kernel may be scheduled as SMs free up; it waits for this grid's end.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -377,21 +372,26 @@ __global__ void __launch_bounds__(Tile<PROMOTE>::kThreads, 1) linear_tc_kernel(
         const TileAt mn = tile_at(pc.tile, mt, nt);
         const int m0 = mn.m * (2 * kRows) + rank * kRows;
         const int n0 = mn.n * BN + rank * kCols;
-        const int kblocks = pc.kb1 - pc.kb0, seg = segment(kblocks);
-        Step at;
-        for (int i = 0; i < kblocks * products; ++i, at.advance(kblocks, seg, products)) {
+        for (int kb = pc.kb0; kb < pc.kb1 && ok; ++kb) {
+          const int k0 = kb * kK;
+          for (int i = 0; i < nsteps; ++i) {
+          const int what = AP > 1 ? step_planes(steps, i) : 0x1000;
+          const int count = AP > 1 ? what >> 12 : 1, pb = (what >> 8) & 15;
           if (!mbar_wait(&empty[s], ph ^ 1, status, abort)) { ok = false; break; }
           uint8_t* a = stages + s * T::kStage;
-          uint8_t* b = a + kABytes;
-          const int k0 = (pc.kb0 + at.kb) * kK;
-          const int pa = (a_planes >> (4 * at.pair)) & 15, pb = (b_planes >> (4 * at.pair)) & 15;
+          uint8_t* b = a + AP * kABytes;
           const uint32_t bar = leader_addr(&full[s]);
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * T::kStage);
-          if (A_MN) {
-            tma_load_3d_pair(a, &tm_a, bar, m0, k0, pa);
-            tma_load_3d_pair(a + kMnBlock, &tm_a, bar, m0 + 64, k0, pa);
-          } else {
-            tma_load_3d_pair(a, &tm_a, bar, k0, m0, pa);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (count * kABytes + T::kBBytes));
+#pragma unroll
+          for (int p = 0; p < AP; ++p) {
+            if (p >= count) break;
+            const int pa = (what >> (4 * p)) & 15;
+            if (A_MN) {
+              tma_load_3d_pair(a + p * kABytes, &tm_a, bar, m0, k0, pa);
+              tma_load_3d_pair(a + p * kABytes + kMnBlock, &tm_a, bar, m0 + 64, k0, pa);
+            } else {
+              tma_load_3d_pair(a + p * kABytes, &tm_a, bar, k0, m0, pa);
+            }
           }
           if (B_MN) {
 #pragma unroll
@@ -402,6 +402,7 @@ __global__ void __launch_bounds__(Tile<PROMOTE>::kThreads, 1) linear_tc_kernel(
           }
           ++issued;
           if (++s == T::kStages) { s = 0; ph ^= 1; }
+          }
         }
       }
       if (!ok) {
@@ -432,23 +433,31 @@ __global__ void __launch_bounds__(Tile<PROMOTE>::kThreads, 1) linear_tc_kernel(
       while (ok && work.next(&pc)) {
         const int kblocks = pc.kb1 - pc.kb0, seg = segment(kblocks);
         for (int k = 0; k < kblocks && ok; k += seg, ++it) {
-          const int here = min(seg, kblocks - k) * products;
+          const int here = min(seg, kblocks - k) * nsteps;
           const int buf = it & 1;
           const uint32_t tph = (it >> 1) & 1;
           if (!mbar_wait(&tempty[buf], tph ^ 1, status, abort)) { ok = false; break; }
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + buf * BN;
+          int step = 0;
           for (int i = 0; i < here; ++i) {
+            const int count = AP > 1 ? step_planes(steps, step) >> 12 : 1;
+            if (++step == nsteps) step = 0;
             if (!mbar_wait(&full[s], ph, status, abort)) { ok = false; break; }
             tc_fence_after();
             const uint32_t a = smem_addr(stages + s * T::kStage);
-            const uint32_t b = a + kABytes;
+            const uint32_t b = a + AP * kABytes;
 #pragma unroll
-            for (int j = 0; j < kK / 16; ++j) {
-              // 16 K = two 8-row atoms of an MN-major tile, 32 bytes of a K-major row.
-              const uint64_t ad = A_MN ? mn_desc(a + j * 2048) : sw128_desc(a, j * 32);
-              const uint64_t bd = B_MN ? mn_desc(b + j * 2048) : sw128_desc(b, j * 32);
-              mma_bf16_pair(d_tmem, ad, bd, idesc, (i != 0 || j != 0) ? 1u : 0u);
+            for (int p = 0; p < AP; ++p) {
+              if (p >= count) break;
+#pragma unroll
+              for (int j = 0; j < kK / 16; ++j) {
+                // 16 K = two 8-row atoms of an MN-major tile, 32 bytes of a K-major row.
+                const uint32_t ap = a + p * kABytes;
+                const uint64_t ad = A_MN ? mn_desc(ap + j * 2048) : sw128_desc(ap, j * 32);
+                const uint64_t bd = B_MN ? mn_desc(b + j * 2048) : sw128_desc(b, j * 32);
+                mma_bf16_pair(d_tmem, ad, bd, idesc, (i != 0 || p != 0 || j != 0) ? 1u : 0u);
+              }
             }
             mma_commit_pair(&empty[s]);
             if (++s == T::kStages) { s = 0; ph ^= 1; }
@@ -605,9 +614,9 @@ bool output_map(CUtensorMap* m, const void* p, bool f32, int64_t cols, int64_t r
                   f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 }
 
-template <bool A_MN, bool B_MN, bool PROMOTE>
+template <bool A_MN, bool B_MN, int AP, bool PROMOTE>
 cudaError_t run(const LinearGemm& g, int* launches, cudaStream_t st) {
-  using T = Tile<PROMOTE>;
+  using T = Tile<AP, PROMOTE>;
   CUtensorMap tm_a, tm_b;
   // K-major: [planes][rows][K]; MN-major: [planes][K][columns]; ld elements a row.
   const cuuint64_t al = static_cast<cuuint64_t>(g.lda) * 2, bl = static_cast<cuuint64_t>(g.ldb) * 2;
@@ -628,7 +637,7 @@ cudaError_t run(const LinearGemm& g, int* launches, cudaStream_t st) {
       (tma && e.pre && !output_map(&tm_pre, e.pre, e.pre_f32, g.N, g.M, 1)) ||
       (g.part && !output_map(&tm_part, g.part, true, BN, 2 * kRows, 2 * g.work.pairs)))
     return cudaErrorInvalidValue;
-  auto* kernel = linear_tc_kernel<A_MN, B_MN, PROMOTE>;
+  auto* kernel = linear_tc_kernel<A_MN, B_MN, AP, PROMOTE>;
   cudaError_t rc = set_max_smem(reinterpret_cast<const void*>(kernel), T::kSmem);
   if (rc != cudaSuccess) return rc;
   cudaLaunchConfig_t cfg = {};
@@ -643,8 +652,8 @@ cudaError_t run(const LinearGemm& g, int* launches, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  rc = cudaLaunchKernelEx(&cfg, kernel, tm_a, tm_b, tm_y, tm_pre, tm_part, g.M, g.N, g.a_planes,
-                          g.b_planes, g.products, g.work, tma, g.epi, g.status, g.clear);
+  rc = cudaLaunchKernelEx(&cfg, kernel, tm_a, tm_b, tm_y, tm_pre, tm_part, g.M, g.N,
+                          g.steps.packed, g.steps.count, g.work, tma, g.epi, g.status, g.clear);
   if (rc != cudaSuccess) return rc;
   ++*launches;
   if (!g.part) return cudaSuccess;
@@ -664,9 +673,10 @@ cudaError_t run(const LinearGemm& g, int* launches, cudaStream_t st) {
 
 template <bool A_MN, bool B_MN>
 cudaError_t promoted(const LinearGemm& g, int* launches, cudaStream_t st) {
+  if (g.steps.products > 1) return run<A_MN, B_MN, 2, true>(g, launches, st);
   // fp32 results; a bf16 result's own rounding hides the cuts.
-  return g.epi.y_f32 || (g.epi.pre && g.epi.pre_f32) ? run<A_MN, B_MN, true>(g, launches, st)
-                                                     : run<A_MN, B_MN, false>(g, launches, st);
+  return g.epi.y_f32 || (g.epi.pre && g.epi.pre_f32) ? run<A_MN, B_MN, 1, true>(g, launches, st)
+                                                     : run<A_MN, B_MN, 1, false>(g, launches, st);
 }
 
 }  // namespace
