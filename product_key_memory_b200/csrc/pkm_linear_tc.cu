@@ -35,11 +35,12 @@
 // smallest products first.
 //
 // Epilogue: with PROMOTE 8 warps (two per TMEM lane quadrant; their accumulators take the
-// registers), else up to 16, whose activations hide one another's latencies. A thread owns
-// a row of 32 columns at a time. Rows go through shared memory,
-// swizzled, and leave as TMA stores of 32 x 32 (a thread's own 16-byte stores would touch
-// a line per lane); outputs whose rows are no multiple of 16 bytes go out a row at a
-// time, lanes along the columns.
+// registers), else 16, whose activations hide one another's latencies. A thread owns a row
+// of 32 columns at a time. Rows go through shared memory, swizzled, and leave as TMA
+// stores of 32 rows x 128 bytes (a thread's own 16-byte stores would touch a line per
+// lane); for `pre` and y of bf16 outputs the accumulator is read twice, so that one buffer
+// serves both. Outputs whose rows are no multiple of 16 bytes go out a row at a time, lanes
+// along the columns.
 #include "pkm_linear_epi.cuh"
 #include "pkm_tc.h"
 #include "pkm_tcgen05.cuh"
@@ -224,6 +225,29 @@ struct Outputs {
   bool tma;              // rows are multiples of 16 bytes
 };
 
+__device__ __forceinline__ void add_bias32(const float* bias, int col, int N, float* v) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    if (col + i < N) {   // N is a multiple of 4
+      const float4 b = __ldg(reinterpret_cast<const float4*>(bias + col + i));
+      v[i] += b.x; v[i + 1] += b.y; v[i + 2] += b.z; v[i + 3] += b.w;
+    }
+  }
+}
+
+__device__ __forceinline__ void activate32(int act, float* v) {
+  if (act == PKM_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], PKM_ACT_RELU);
+  } else if (act == PKM_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], PKM_ACT_GELU);
+  } else if (act == PKM_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], PKM_ACT_SILU);
+  }
+}
+
 // 32 rows x 32 columns of the result: this thread's row `row0 + lane` in v, columns from
 // `col`. Warp-uniform arguments but v.
 __device__ __forceinline__ void store_block(const CUtensorMap* tm_y, const CUtensorMap* tm_pre,
@@ -239,26 +263,9 @@ __device__ __forceinline__ void store_block(const CUtensorMap* tm_y, const CUten
     o.part_before = false;
     __syncwarp();
     if (e.residual) stage_residual(y, e.residual, e.y_f32, row0, col, M, N, lane);
-    if (e.bias) {
-#pragma unroll
-      for (int i = 0; i < 32; i += 4) {
-        if (col + i < N) {   // N is a multiple of 4
-          const float4 b = __ldg(reinterpret_cast<const float4*>(e.bias + col + i));
-          v[i] += b.x; v[i + 1] += b.y; v[i + 2] += b.z; v[i + 3] += b.w;
-        }
-      }
-    }
+    if (e.bias) add_bias32(e.bias, col, N, v);
     if (e.pre) stage_row(p, lane, e.pre_f32, v);
-    if (e.act == PKM_ACT_RELU) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], PKM_ACT_RELU);
-    } else if (e.act == PKM_ACT_GELU) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], PKM_ACT_GELU);
-    } else if (e.act == PKM_ACT_SILU) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], PKM_ACT_SILU);
-    }
+    activate32(e.act, v);
     if (e.residual) {
       __syncwarp();   // the other lanes' chunks of this row
       add_residual(y, lane, e.y_f32, v);
@@ -289,6 +296,69 @@ __device__ __forceinline__ void store_block(const CUtensorMap* tm_y, const CUten
       linear_store1(e, static_cast<int64_t>(row0 + r) * N + col + lane, col + lane,
                     lds_f32(base + (r * 32 + (lane ^ r)) * 4));
   }
+}
+
+// 32 rows x 64 columns of bf16 outputs of a whole tile, straight from TMEM columns `tmem`: the
+// columns' first 32, then the others, staged as 128-byte rows. `release` is called once the
+// accumulator has been read for the last time.
+template <typename Release>
+__device__ __forceinline__ void store_block64(uint32_t tmem, const CUtensorMap* tm_y,
+                                              const CUtensorMap* tm_pre, const LinearEpilogue& e,
+                                              Outputs& o, int row0, int col, int M, int N, int lane,
+                                              const Release& release) {
+  for (int pass = e.pre ? 0 : 1; pass < 2; ++pass) {
+    if (lane == 0) bulk_wait_read0();   // the buffer's last store has left it
+    __syncwarp();
+    if (pass && e.residual) {
+      const int c = lane & 7;           // 16-byte chunk of a row
+      for (int r = lane >> 3; r < 32; r += 4) {
+        uint4 q = make_uint4(0, 0, 0, 0);
+        if (row0 + r < M && col + c * 8 < N)
+          q = *reinterpret_cast<const uint4*>(
+              static_cast<const uint16_t*>(e.residual) +
+              static_cast<int64_t>(row0 + r) * N + col + c * 8);
+        sts128(tile_chunk(o.staging, r, c, true), q.x, q.y, q.z, q.w);
+      }
+      __syncwarp();
+    }
+#pragma unroll 1
+    for (int g = 0; g < 2; ++g) {
+      float v[32];
+      __syncwarp();
+      tmem_ld32(tmem + g * 32, v);
+      if (pass && g) release();
+      if (col + g * 32 >= N) continue;
+      if (e.bias) add_bias32(e.bias, col + g * 32, N, v);
+      if (pass) {
+        activate32(e.act, v);
+        if (e.residual) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float4 q = lds128(tile_chunk(o.staging, lane, g * 4 + c, true));
+            const uint32_t w[4] = {__float_as_uint(q.x), __float_as_uint(q.y), __float_as_uint(q.z),
+                                   __float_as_uint(q.w)};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              v[8 * c + 2 * k] += bf16_lo(w[k]);
+              v[8 * c + 2 * k + 1] += bf16_hi(w[k]);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c)   // a row that this thread alone has read
+        sts128(tile_chunk(o.staging, lane, g * 4 + c, true), pack_bf16(v[8 * c], v[8 * c + 1]),
+               pack_bf16(v[8 * c + 2], v[8 * c + 3]), pack_bf16(v[8 * c + 4], v[8 * c + 5]),
+               pack_bf16(v[8 * c + 6], v[8 * c + 7]));
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_3d_at(pass ? tm_y : tm_pre, o.staging, col, row0, 0);
+      bulk_commit();
+    }
+  }
+  o.part_before = true;   // the buffer is single here
 }
 
 // The same block of a part: fp32 as it is, at (col, row) of the part's 256 x BN.
@@ -520,6 +590,13 @@ __global__ void __launch_bounds__(Tile<AP, PROMOTE>::kThreads, 1) linear_tc_kern
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(leader_addr(&tempty[buf]));
+        } else if (o.tma && pc.slot < 0 && row0 < M && n0 < N) {
+          static_assert(PROMOTE || kGroups == 2, "64 columns a warp");
+          store_block64(d_tmem, &tm_y, &tm_pre, epi, o, row0, n0, M, N, lane, [&] {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(leader_addr(&tempty[buf]));
+          });
         } else {
 #pragma unroll 1
           for (int g = 0; g < kGroups; ++g) {
@@ -603,14 +680,16 @@ __global__ void __launch_bounds__(kJoinRows* BN / 8) linear_join_kernel(
 }
 
 // [planes][rows][cols] of an output or of the parts.
-bool output_map(CUtensorMap* m, const void* p, bool f32, int64_t cols, int64_t rows, int planes) {
+bool output_map(CUtensorMap* m, const void* p, bool f32, int64_t cols, int64_t rows, int planes,
+                int box_cols = 32) {
   const cuuint64_t e = f32 ? 4 : 2;
   const cuuint64_t d[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                            static_cast<cuuint64_t>(planes)};
   const cuuint64_t s[2] = {static_cast<cuuint64_t>(cols) * e,
                            static_cast<cuuint64_t>(cols * rows) * e};
-  const cuuint32_t b[3] = {32, 32, 1};
-  return make_map(m, p, 3, d, s, b, f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+  const cuuint32_t b[3] = {static_cast<cuuint32_t>(box_cols), 32, 1};
+  return make_map(m, p, 3, d, s, b,
+                  box_cols * e == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                   f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 }
 
@@ -633,8 +712,9 @@ cudaError_t run(const LinearGemm& g, int* launches, cudaStream_t st) {
   const LinearEpilogue& e = g.epi;
   const int tma = g.N % (e.y_f32 ? 4 : 8) == 0 && (!e.pre || e.pre_f32 || g.N % 8 == 0);
   CUtensorMap tm_y = tm_a, tm_pre = tm_a, tm_part = tm_a;
-  if ((tma && !output_map(&tm_y, e.y, e.y_f32, g.N, g.M, 1)) ||
-      (tma && e.pre && !output_map(&tm_pre, e.pre, e.pre_f32, g.N, g.M, 1)) ||
+  const int box = PROMOTE ? 32 : 64;   // columns stored at a time
+  if ((tma && !output_map(&tm_y, e.y, e.y_f32, g.N, g.M, 1, box)) ||
+      (tma && e.pre && !output_map(&tm_pre, e.pre, e.pre_f32, g.N, g.M, 1, box)) ||
       (g.part && !output_map(&tm_part, g.part, true, BN, 2 * kRows, 2 * g.work.pairs)))
     return cudaErrorInvalidValue;
   auto* kernel = linear_tc_kernel<A_MN, B_MN, AP, PROMOTE>;
