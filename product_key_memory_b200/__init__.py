@@ -479,8 +479,14 @@ class _Call:
         if self.guard is not None:
             self.guard.__exit__(*exc)
 
-    def empty(self, shape, dtype) -> torch.Tensor:
-        t = torch.empty(shape, dtype=dtype, device=self.device)
+    def empty(self, like: torch.Tensor, shape, dtype) -> torch.Tensor:
+        """An uninitialised tensor beside `like` (the forms that cost the host least)."""
+        if dtype is not like.dtype:
+            t = like.new_empty(shape, dtype=dtype)
+        elif shape == like.shape:
+            t = torch.empty_like(like)
+        else:
+            t = like.new_empty(shape)
         if self.given is not None:
             t.record_stream(self.given)
         return t
@@ -546,11 +552,11 @@ def pkm_layernorm_forward(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[t
                        eps)
     with _Call(dev, stream) as c:
         if out is None:
-            out = c.empty((rows, d), out_dtype)
+            out = c.empty(x, (rows, d), out_dtype)
         if sum_out is None and add is not None:
-            sum_out = c.empty((rows, d), x.dtype)
-        mean = c.empty(rows, torch.float32) if want_stats else None
-        rstd = c.empty(rows, torch.float32) if want_stats else None
+            sum_out = c.empty(x, (rows, d), x.dtype)
+        mean = c.empty(gamma, (rows,), torch.float32) if want_stats else None
+        rstd = c.empty(gamma, (rows,), torch.float32) if want_stats else None
         rc = lib().pkm_layernorm_forward(ref, _addr(x), _addr(add), _addr(gamma),
                                          _addr(beta), _addr(out), _addr(sum_out), _addr(mean),
                                          _addr(rstd), c.handle)
@@ -595,13 +601,13 @@ def pkm_layernorm_backward(grad_y: torch.Tensor, x: torch.Tensor, mean: torch.Te
                           grad_y.dtype, grad_dtype)
     with _Call(dev, stream) as c:
         if grad_x is None:
-            grad_x = c.empty((rows, d), grad_dtype)
+            grad_x = c.empty(x, (rows, d), grad_dtype)
         if grad_gamma is None:
-            grad_gamma = c.empty(d, torch.float32)
+            grad_gamma = c.empty(gamma, (d,), torch.float32)
         if grad_beta is None:
-            grad_beta = c.empty(d, torch.float32)
+            grad_beta = c.empty(gamma, (d,), torch.float32)
         if workspace is None:
-            workspace = c.empty(max(need, 1), torch.uint8)
+            workspace = c.empty(x, (max(need, 1),), torch.uint8)
         ws, nbytes = _given_workspace(c, workspace)
         rc = lib().pkm_layernorm_backward(ref, _addr(grad_y), _addr(x),
                                           _addr(mean), _addr(rstd), _addr(gamma), _addr(grad_sum),
@@ -749,10 +755,10 @@ def _linear_ref(for_backward, *fields):
     return ref, int(lib().pkm_linear_workspace_size(ref, for_backward))
 
 
-def _linear_workspace(c: _Call, workspace, need: int):
+def _linear_workspace(c: _Call, x, workspace, need: int):
     """(workspace, bytes): the caller's, or one for this call."""
     if workspace is None:
-        return c.empty(max(need, 1), torch.uint8), need
+        return c.empty(x, (max(need, 1),), torch.uint8), need
     return _given_workspace(c, workspace)
 
 
@@ -792,10 +798,10 @@ def pkm_linear_forward(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Te
     ref, need = _linear_ref(0, M, N, K, x.dtype, out_dtype, act)
     with _Call(dev, stream) as c:
         if out is None:
-            out = c.empty((M, N), out_dtype)
+            out = c.empty(x, (M, N), out_dtype)
         if pre is None and want_pre:
-            pre = c.empty((M, N), x.dtype)
-        ws, nbytes = _linear_workspace(c, workspace, need)
+            pre = c.empty(x, (M, N), x.dtype)
+        ws, nbytes = _linear_workspace(c, x, workspace, need)
         rc = lib().pkm_linear_forward(ref, _addr(x), _addr(W), _addr(bias),
                                       _addr(residual), _addr(out), _addr(pre),
                                       _addr(ws), nbytes, c.handle)
@@ -829,7 +835,7 @@ def pkm_linear_backward(x: torch.Tensor, W: torch.Tensor, grad_y: torch.Tensor, 
         _check("grads['bias']", gb, (N,), torch.float32, dev)
     ref, need = _linear_ref(1, M, N, K, x.dtype, x.dtype if gx is None else gx.dtype, act)
     with _Call(dev, stream) as c:
-        ws, nbytes = _linear_workspace(c, workspace, need)
+        ws, nbytes = _linear_workspace(c, x, workspace, need)
         rc = lib().pkm_linear_backward(ref, _addr(x), _addr(W), _addr(grad_y),
                                        _addr(pre), _addr(gx), _addr(gW), _addr(gb),
                                        _addr(ws), nbytes, c.handle)

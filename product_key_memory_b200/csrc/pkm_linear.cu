@@ -29,6 +29,8 @@ template <typename E, int V, int M>
 __global__ void __launch_bounds__(256) linear_small_kernel(const void* x, const void* W, int N,
                                                            int K, const LinearEpilogue epi,
                                                            int* status) {
+  let_next_in();
+  wait_for_previous();
   clear_status(status);
   const int lane = threadIdx.x & 31;
   const int col = blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -71,14 +73,19 @@ template <typename E, int V>
 cudaError_t run_small(int M, const void* x, const void* W, int N, int K,
                       const LinearEpilogue& epi, int* status, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>((N + 7) / 8);
+  const auto run = [&](auto* kernel) {
+    return launch_after(kernel, grid, 256, 0, 1, st, x, W, N, K, epi, status);
+  };
   switch (M) {
-#define PKM_CASE(m) \
-  case m: linear_small_kernel<E, V, m><<<grid, 256, 0, st>>>(x, W, N, K, epi, status); break;
-    PKM_CASE(1) PKM_CASE(2) PKM_CASE(3) PKM_CASE(4) PKM_CASE(5) PKM_CASE(6) PKM_CASE(7)
-    default: linear_small_kernel<E, V, 8><<<grid, 256, 0, st>>>(x, W, N, K, epi, status);
-#undef PKM_CASE
+    case 1: return run(linear_small_kernel<E, V, 1>);
+    case 2: return run(linear_small_kernel<E, V, 2>);
+    case 3: return run(linear_small_kernel<E, V, 3>);
+    case 4: return run(linear_small_kernel<E, V, 4>);
+    case 5: return run(linear_small_kernel<E, V, 5>);
+    case 6: return run(linear_small_kernel<E, V, 6>);
+    case 7: return run(linear_small_kernel<E, V, 7>);
+    default: return run(linear_small_kernel<E, V, 8>);
   }
-  return cudaGetLastError();
 }
 
 // --------------------------------------------------------------- operand planes
@@ -136,39 +143,46 @@ __device__ __forceinline__ void store_planes(uint16_t* dst, int64_t plane, int64
   for (int n = 0; n < NP; ++n) Out<BF16, 8>::store(dst + n * plane, at, p[n]);
 }
 
-// [rows][cols] of E -> NP planes [rows][ld] of bf16, ld a multiple of 8.
+// [rows][cols] of E -> NP planes [rows][ld] of bf16, ld a multiple of 8; two arrays of as many
+// columns at a time (the second may have no rows).
+struct PlanesOf {
+  const void* src;
+  uint16_t* dst;
+  int64_t rows;
+};
 template <typename E, int V, int NP>
-__global__ void __launch_bounds__(256) linear_planes_kernel(const void* src, uint16_t* dst,
-                                                            int64_t rows, int cols, int64_t ld,
-                                                            int* status) {
+__global__ void __launch_bounds__(256) linear_planes_kernel(const PlanesOf a, const PlanesOf b,
+                                                            int cols, int64_t ld, int* status) {
+  let_next_in();
+  wait_for_previous();
   clear_status(status);
   const int chunks = static_cast<int>(ld / 8);
-  const int64_t total = rows * chunks;
+  const int64_t total = (a.rows + b.rows) * chunks;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
        i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t r = i / chunks;
+    int64_t r = i / chunks;
     const int col = static_cast<int>(i - r * chunks) * 8;
+    const bool second = r >= a.rows;
+    if (second) r -= a.rows;
+    const int64_t rows = second ? b.rows : a.rows;
     float f[8];
     Chunk<E, V> c;
-    c.load(src, r * cols + col, col, cols);
+    c.load(second ? b.src : a.src, r * cols + col, col, cols);
     c.get(f);
-    store_planes<NP>(dst, rows * ld, r * ld + col, f);
+    store_planes<NP>(second ? b.dst : a.dst, rows * ld, r * ld + col, f);
   }
 }
 
-cudaError_t make_planes(const void* src, int dtype, uint16_t* dst, int64_t rows, int cols,
-                        int* status, cudaStream_t st) {
+cudaError_t make_planes(const PlanesOf& a, const PlanesOf& b, int dtype, int cols, int* status,
+                        cudaStream_t st) {
   const int64_t ld = pad8(cols);
-  const int64_t blocks = (rows * (ld / 8) + 255) / 256;
+  const int64_t blocks = ((a.rows + b.rows) * (ld / 8) + 255) / 256;
   const unsigned grid = static_cast<unsigned>(blocks < 148 * 32 ? blocks : 148 * 32);
   const bool vec = cols % 8 == 0;
-  if (dtype == PKM_F32) {
-    if (vec) linear_planes_kernel<F32, 8, 3><<<grid, 256, 0, st>>>(src, dst, rows, cols, ld, status);
-    else linear_planes_kernel<F32, 1, 3><<<grid, 256, 0, st>>>(src, dst, rows, cols, ld, status);
-  } else {
-    linear_planes_kernel<BF16, 1, 1><<<grid, 256, 0, st>>>(src, dst, rows, cols, ld, status);
-  }
-  return cudaGetLastError();
+  auto* kernel = dtype == PKM_BF16 ? linear_planes_kernel<BF16, 1, 1>
+                 : vec             ? linear_planes_kernel<F32, 8, 3>
+                                   : linear_planes_kernel<F32, 1, 3>;
+  return launch_after(kernel, grid, 256, 0, 1, st, a, b, cols, ld, status);
 }
 
 // ------------------------------------------------------------ d = grad_y act'(pre)
@@ -184,6 +198,8 @@ __global__ void __launch_bounds__(256) linear_slope_kernel(const void* gy, const
                                                            int64_t rows, int cols, int64_t ld,
                                                            int* status) {
   __shared__ float sh[8][256];
+  let_next_in();
+  wait_for_previous();
   clear_status(status);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.y * 256 + lane * 8;
@@ -230,8 +246,10 @@ __global__ void __launch_bounds__(256) linear_slope_kernel(const void* gy, const
   }
 }
 
-__global__ void __launch_bounds__(256) linear_bias_kernel(const float* __restrict__ part, int64_t blocks,
+__global__ void __launch_bounds__(256) linear_bias_kernel(const float* part, int64_t blocks,
                                                           int cols, float* out) {
+  let_next_in();
+  wait_for_previous();
   __shared__ float sh[8][33];
   const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + c;
@@ -254,24 +272,11 @@ cudaError_t run_slope(int planes, const void* gy, const void* pre, int act, uint
   const dim3 grid(static_cast<unsigned>((rows + kPrepRows - 1) / kPrepRows),
                   static_cast<unsigned>((cols + 255) / 256));
   const int64_t ld = pad8(cols);
-  switch (planes) {
-    case 0:
-      linear_slope_kernel<E, V, 0><<<grid, 256, 0, st>>>(gy, pre, act, dst, part, rows, cols, ld,
-                                                          status);
-      break;
-    case 1:
-      linear_slope_kernel<E, V, 1><<<grid, 256, 0, st>>>(gy, pre, act, dst, part, rows, cols, ld,
-                                                          status);
-      break;
-    case 2:
-      linear_slope_kernel<E, V, 2><<<grid, 256, 0, st>>>(gy, pre, act, dst, part, rows, cols, ld,
-                                                          status);
-      break;
-    default:
-      linear_slope_kernel<E, V, 3><<<grid, 256, 0, st>>>(gy, pre, act, dst, part, rows, cols, ld,
-                                                          status);
-  }
-  return cudaGetLastError();
+  auto* kernel = planes == 0   ? linear_slope_kernel<E, V, 0>
+                 : planes == 1 ? linear_slope_kernel<E, V, 1>
+                 : planes == 2 ? linear_slope_kernel<E, V, 2>
+                               : linear_slope_kernel<E, V, 3>;
+  return launch_after(kernel, grid, 256, 0, 1, st, gy, pre, act, dst, part, rows, cols, ld, status);
 }
 
 // ------------------------------------------------------------------- host side
@@ -402,14 +407,13 @@ cudaError_t launch_linear_forward(const LinearArgs& a, const void* x, const void
   char* ws = static_cast<char*>(workspace);
   const int64_t ld = pad8(a.K);
   if (!in_place(a.dtype, a.K)) {
-    e = make_planes(x, a.dtype, reinterpret_cast<uint16_t*>(ws + l.x), a.M, a.K, first, st);
-    if (e == cudaSuccess)
-      e = make_planes(W, a.dtype, reinterpret_cast<uint16_t*>(ws + l.W), a.N, a.K, nullptr, st);
+    e = make_planes({x, reinterpret_cast<uint16_t*>(ws + l.x), a.M},
+                    {W, reinterpret_cast<uint16_t*>(ws + l.W), a.N}, a.dtype, a.K, first, st);
     if (e != cudaSuccess) return e;
     first = nullptr;
     x = ws + l.x;
     W = ws + l.W;
-    *launches += 2;
+    ++*launches;
   }
   const uint32_t in = static_cast<uint32_t>(input_planes(a.dtype));
   const LinearGemm g{kForward, x, W, ld, ld, static_cast<int>(a.M), a.N, a.K, in, in, l.fwd_p, l.fwd,
@@ -445,9 +449,8 @@ cudaError_t launch_linear_backward(const LinearArgs& a, const void* x, const voi
     first = nullptr;
     ++*launches;
     if (grad_bias) {
-      linear_bias_kernel<<<(a.N + 31) / 32, 256, 0, st>>>(
-          part, (a.M + kPrepRows - 1) / kPrepRows, a.N, grad_bias);
-      e = cudaGetLastError();
+      e = launch_after(linear_bias_kernel, (a.N + 31) / 32, 256, 0, 1, st, part,
+                       (a.M + kPrepRows - 1) / kPrepRows, a.N, grad_bias);
       if (e != cudaSuccess) return e;
       ++*launches;
     }
@@ -457,14 +460,17 @@ cudaError_t launch_linear_backward(const LinearArgs& a, const void* x, const voi
   const uint32_t dcount = dp ? dp : 1, in = static_cast<uint32_t>(input_planes(a.dtype));
   const bool inpl = in_place(a.dtype, a.K);
   float* part = reinterpret_cast<float*>(ws + l.part);
+  if (!inpl) {   // W's planes for grad_x, x's for grad_W
+    e = make_planes({W, reinterpret_cast<uint16_t*>(ws + l.W), grad_x ? a.N : 0},
+                    {x, reinterpret_cast<uint16_t*>(ws + l.x), grad_W ? a.M : 0}, a.dtype, a.K,
+                    first, st);
+    if (e != cudaSuccess) return e;
+    first = nullptr;
+    W = ws + l.W;
+    x = ws + l.x;
+    ++*launches;
+  }
   if (grad_x) {
-    if (!inpl) {
-      e = make_planes(W, a.dtype, reinterpret_cast<uint16_t*>(ws + l.W), a.N, a.K, first, st);
-      if (e != cudaSuccess) return e;
-      first = nullptr;
-      W = ws + l.W;
-      ++*launches;
-    }
     const LinearEpilogue epi{grad_x, nullptr, nullptr, nullptr, a.out_dtype == PKM_F32, 0,
                              PKM_ACT_NONE};
     const LinearGemm g{kGradX, dop, W, ldn, ldk, static_cast<int>(a.M), a.K, a.N, dcount, in,
@@ -475,13 +481,6 @@ cudaError_t launch_linear_backward(const LinearArgs& a, const void* x, const voi
     first = nullptr;
   }
   if (grad_W) {
-    if (!inpl) {
-      e = make_planes(x, a.dtype, reinterpret_cast<uint16_t*>(ws + l.x), a.M, a.K, first, st);
-      if (e != cudaSuccess) return e;
-      first = nullptr;
-      x = ws + l.x;
-      ++*launches;
-    }
     const LinearEpilogue epi{grad_W, nullptr, nullptr, nullptr, 1, 0, PKM_ACT_NONE};
     const LinearGemm g{kGradW, dop, x, ldn, ldk, a.N, a.K, static_cast<int>(a.M), dcount, in,
                        l.gw_p, l.gw, l.gw.cut ? part : nullptr, epi,

@@ -402,11 +402,9 @@ __global__ void __launch_bounds__(Tile<AP, PROMOTE>::kThreads, 1) linear_tc_kern
   const int pair = blockIdx.x >> 1;
   // Segments of a piece of k K blocks.
   const auto segment = [](int k) { return PROMOTE ? (AP > 1 ? kSegment / 2 : kSegment) : k; };
-  // The join kernel may be scheduled as SMs free up; it waits for this grid's end.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_in();
 
   if (threadIdx.x == 0) {
-    if (clear && blockIdx.x == 0) *status = 0;
     for (int s = 0; s < T::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -429,6 +427,9 @@ __global__ void __launch_bounds__(Tile<AP, PROMOTE>::kThreads, 1) linear_tc_kern
   cluster_sync_all();   // the peer's barriers too
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  // The set-up above ran beside the previous kernel's end; global memory starts here.
+  wait_for_previous();
+  if (clear && blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -651,7 +652,8 @@ __global__ void __launch_bounds__(kJoinRows* BN / 8) linear_join_kernel(
   const int c0 = plan.owner(p0), c1 = plan.owner(p1 - 1);
   // The first pair's part is its second one when its range began in an earlier tile.
   const int first = 2 * c0 + (plan.begin(c0) >= p0 ? 0 : 1);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  let_next_in();
+  wait_for_previous();
   if (m >= M || n >= N || c0 == c1) return;              // c0 == c1: one pair had it all
   constexpr int64_t kPart = static_cast<int64_t>(2 * kRows) * BN;
   const float* q = part + static_cast<int64_t>(row) * BN + col;
@@ -720,35 +722,17 @@ cudaError_t run(const LinearGemm& g, int* launches, cudaStream_t st) {
   auto* kernel = linear_tc_kernel<A_MN, B_MN, AP, PROMOTE>;
   cudaError_t rc = set_max_smem(reinterpret_cast<const void*>(kernel), T::kSmem);
   if (rc != cudaSuccess) return rc;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * g.work.pairs);
-  cfg.blockDim = dim3(T::kThreads);
-  cfg.dynamicSmemBytes = T::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  rc = cudaLaunchKernelEx(&cfg, kernel, tm_a, tm_b, tm_y, tm_pre, tm_part, g.M, g.N,
-                          g.steps.packed, g.steps.count, g.work, tma, g.epi, g.status, g.clear);
+  rc = launch_after(kernel, dim3(2 * g.work.pairs), dim3(T::kThreads), T::kSmem, 2, st, tm_a, tm_b,
+                    tm_y, tm_pre, tm_part, g.M, g.N, g.steps.packed, g.steps.count, g.work, tma,
+                    g.epi, g.status, g.clear);
   if (rc != cudaSuccess) return rc;
   ++*launches;
   if (!g.part) return cudaSuccess;
   const int mt = (g.M + 2 * kRows - 1) / (2 * kRows), nt = (g.N + BN - 1) / BN;
-  cudaLaunchConfig_t jc = {};
-  jc.gridDim = dim3(static_cast<unsigned>((mt * nt - g.work.whole) * (2 * kRows / kJoinRows)));
-  jc.blockDim = dim3(kJoinRows * BN / 8);
-  jc.stream = st;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  jc.attrs = attr;
-  jc.numAttrs = 1;
+  const unsigned blocks = static_cast<unsigned>((mt * nt - g.work.whole) * (2 * kRows / kJoinRows));
   ++*launches;
-  return cudaLaunchKernelEx(&jc, linear_join_kernel, static_cast<const float*>(g.part), g.work,
-                            mt, nt, g.M, g.N, g.epi);
+  return launch_after(linear_join_kernel, dim3(blocks), dim3(kJoinRows * BN / 8), 0, 1, st, g.part,
+                      g.work, mt, nt, g.M, g.N, g.epi);
 }
 
 template <bool A_MN, bool B_MN>
