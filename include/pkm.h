@@ -443,15 +443,15 @@ typedef struct {
  * elements (counted from the tensor's start) with its scale s = the smallest power of two,
  * at least 2^-100, with |value| <= 448 s all over the block (NaN where a value is not
  * finite: such a block's states are NaN from then on). A value is code * s. A power of two
- * keeps the codes' grid where it is from one step to the next, so writing an unchanged
- * value again is exact. m / s is rounded to nearest even. One step moves r by a small part
- * of a code, which rounding to nearest would drop every time: q = r / s is rounded to a
- * multiple of ulp, the code spacing at q, after a dither: q / ulp + u to the nearest
- * integer, with u = (b - 32767.5) / 65536, b the 16 low (even elements) or high (odd
- * elements) bits of mix(i / 2 xor key), key = mix(mix(seed + 0x9e3779b9 t) xor
+ * keeps the codes' grid where it is from one step to the next. m / s is rounded to nearest
+ * even. One step moves r by a small part of a code, which rounding to nearest would drop
+ * every time: q = r / s is rounded after a dither, to the code nearest to q + u ulp, with
+ * ulp the code spacing at q and u = (b - 32767.5) / 65536, b the 16 low (even elements) or
+ * high (odd elements) bits of mix(i / 2 xor key), key = mix(mix(seed + 0x9e3779b9 t) xor
  * 0x9e3779b9 index), index the tensor's place in the list, mix MurmurHash3's 32-bit
- * finaliser, all modulo 2^32. What is above 0 stays at least the smallest code, 2^-9. All
- * zeros (codes and scales) are the initial states.
+ * finaliser, all modulo 2^32. (Codes below a power of two lie half as far apart, so a q
+ * within ulp / 4 above one may go to the code below it, half an ulp down.) What is above 0
+ * stays at least the smallest code, 2^-9. All zeros (codes and scales) are the initial states.
  *   dyn: NULL, or three device fp32 {lr, t, grad_scale} read when the step runs, in the
  *        place of hyper's (t a whole number >= 1): a captured step takes new values at
  *        every replay.

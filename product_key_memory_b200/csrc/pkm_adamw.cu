@@ -145,37 +145,26 @@ __device__ __forceinline__ uint2 narrow8(const float* f) {
   return make_uint2(w[0], w[1]);
 }
 
-// The e4m3 code of q = r / s >= 0 rounded to a multiple of ulp, the spacing at q, after the
-// dither u ulp, u = (b - 32767.5) / 65536 from 16 bits of the pair's hash: the nearest
-// multiple of q / ulp + u is the floor of q / ulp + (b + 1/2) / 65536, which is an integer
-// addition of 16 b + 8 to q's bits below the 20 that e4m3 drops. Rounding on q's own grid
-// leaves a q that is a code as it is, powers of two included (the codes below one lie
-// twice as close: rounding q + u ulp to the nearest code would pull such a q down a
-// quarter of the time).
-//
-// For 2^-6 <= q <= 448: 16 times that sum, so that the code is the top byte. `spread` is
-// 16 (16 b + 8) - (960 << 24) modulo 2^32, one byte permutation of the hash (960 is the
-// difference of the exponent biases, in codes).
-__device__ __forceinline__ uint32_t spread_low(uint32_t h) {
-  return __byte_perm(h, 0x40000080u, 0x7104);
+// q = r / s >= 0 with its dither: q + u ulp, ulp being e4m3's spacing at q (2^-9 below 2^-6)
+// and u = (b - 32767.5) / 65536 from 16 bits of the pair's hash, rounded once; the nearest
+// code is taken of it. For two values of 2^-6 <= q at a time.
+__device__ __forceinline__ Pair dithered(Pair q, uint32_t h) {
+  // 2^23 + b as bits; b and u are exact.
+  const Pair b = add(Pair(__uint_as_float(__byte_perm(h, 0x4b000000u, 0x7610)),
+                          __uint_as_float(__byte_perm(h, 0x4b000000u, 0x7632))),
+                     Pair(-8388608.f));
+  const Pair u = fma(b, Pair(1.f / 65536.f), Pair(-32767.5f / 65536.f));
+  const float2 f = q.get();
+  const Pair ulp(__uint_as_float((__float_as_uint(f.x) & 0x7f800000u) - (3u << 23)),
+                 __uint_as_float((__float_as_uint(f.y) & 0x7f800000u) - (3u << 23)));
+  return fma(u, ulp, q);
 }
-__device__ __forceinline__ uint32_t spread_high(uint32_t h) {
-  return __byte_perm(h, 0x40000080u, 0x7324);
-}
-__device__ __forceinline__ uint32_t dithered(float q, uint32_t spread) {   // code in the top byte
-  return __float_as_uint(q) * 16u + spread;
-}
-// Any q, the dither as 16 b + 8. Below 2^-6 the spacing stays 2^-9: there 2^-6 is added first
-// (its ulp is the same) and its code, 8, taken off. 0 for q = 0 alone, at most 448.
-__device__ __forceinline__ uint32_t dithered_any(float q, uint32_t dither) {
-  const bool low = q < 0x1p-6f;
-  const uint32_t bits = __float_as_uint(low ? q + 0x1p-6f : q);
-  const uint32_t c = (bits + dither - (low ? 968u << 20 : 960u << 20)) >> 20;
-  return min(max(c, min(__float_as_uint(q), 1u)), 0x7eu);
-}
-// The top bytes of four words.
-__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+// Any q. What is above 0 stays at least the smallest code.
+__device__ __forceinline__ float dithered_any(float q, uint32_t b16) {
+  const float u = fmaf(static_cast<float>(b16), 1.f / 65536.f, -32767.5f / 65536.f);
+  const uint32_t e = max(__float_as_uint(q) & 0x7f800000u, 121u << 23);
+  const float near = fmaf(u, __uint_as_float(e - (3u << 23)), q);
+  return q > 0.f ? fmaxf(near, 0x1p-9f) : q;
 }
 
 // Eight elements as loaded.
@@ -351,14 +340,14 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
       sr = scale_bits(__float_as_uint(__fsqrt_rn(__uint_as_float(
           __reduce_max_sync(0xffffffffu, __float_as_uint(most_v))))) & 0x7fffffffu);
       // Fast: every r / s is at least 2^-6 (none 2^14 below the block's largest, no zeros) and
-      // at most 448 with the root's error, and 1 / s^2 is a number.
+      // 1 / s^2 is a number.
       const float ir = inverse_pow2(sr), over2 = ir * ir;
       float least = v[0];
 #pragma unroll
       for (int j = 2; j < 8; j += 2) least = min3(least, v[j - 1], v[j]);
       least = fminf(least, v[7]);
       fast = __all_sync(0xffffffffu, least * over2 >= 0x1p-12f && over2 < INFINITY &&
-                                         most_v * over2 < 448.f * 448.f * (1.f - 0x1p-20f));
+                                         most_v < INFINITY);
       if (fast) {
         scale_r = __uint_as_float(sr);
         const Pair o(over2);
@@ -411,33 +400,24 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
       const uint32_t pair = static_cast<uint32_t>(i >> 1);
       const Pair ims(inverse_pow2(sm));
       const float ir = inverse_pow2(sr);
-      uint32_t c[8];
-      uint2 cv;
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
         const Pair q = Pair(m[j], m[j + 1]) * ims;
         m[j] = q.lo(), m[j + 1] = q.hi();
       }
       const uint2 cm = narrow8(m);
-      if (fast) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t h = mix32((pair + j) ^ key);
-          c[2 * j] = dithered(r[2 * j], spread_low(h));
-          c[2 * j + 1] = dithered(r[2 * j + 1], spread_high(h));
+      for (int j = 0; j < 8; j += 2) {
+        const uint32_t h = mix32((pair + j / 2) ^ key);
+        if (fast) {
+          const Pair q = dithered(Pair(r[j], r[j + 1]), h);
+          r[j] = q.lo(), r[j + 1] = q.hi();
+        } else {
+          r[j] = dithered_any(r[j] * ir, h & 0xffffu);
+          r[j + 1] = dithered_any(r[j + 1] * ir, h >> 16);
         }
-        cv = make_uint2(top_bytes(c[0], c[1], c[2], c[3]), top_bytes(c[4], c[5], c[6], c[7]));
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t h = mix32((pair + j) ^ key);
-          c[2 * j] = dithered_any(r[2 * j] * ir, ((h << 4) & 0xffff0u) | 8u);
-          c[2 * j + 1] = dithered_any(r[2 * j + 1] * ir, ((h >> 12) & 0xffff0u) | 8u);
-        }
-        cv = make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24,
-                        c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
       }
-      if (sr == 0x7fc00000u) cv = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);   // a NaN scale's codes
+      const uint2 cv = narrow8(r);                       // saturates at 448
       const int64_t block = i >> 8;
       if (lane == 0) {
         T.ms[block] = __uint_as_float(sm);

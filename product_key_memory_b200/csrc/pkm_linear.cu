@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(256) linear_small_kernel(const void* x, const 
   if (col >= N) return;
   const int64_t base = static_cast<int64_t>(col) * K;
   float acc[M] = {};
-  constexpr int kDepth = 4;
+  constexpr int kDepth = V == 1 ? 16 : 4;
   for (int k0 = lane * V; k0 < K; k0 += 32 * V * kDepth) {
     Raw<E, V> w[kDepth];
 #pragma unroll

@@ -31,8 +31,10 @@
 // 2^-24 of it towards zero, so K / 16 cuts add up (1e-5 of the result at K = 8192). Where
 // the output is fp32 (PROMOTE) the accumulator is therefore taken out every kSegment K
 // blocks and added to fp32 registers, rounded to nearest; the epilogue warps do that while
-// the next segment is multiplied into the other half of TMEM. The steps of a K block go
-// smallest products first.
+// the next segment is multiplied into the other half of TMEM. The steps of a segment go
+// smallest products first, each over all of its K blocks: what the cuts take then is measured
+// against the small sums for all but the last step (one K block after the other, all of its
+// steps, left an fp32 result at 1.3e-6 instead of 3e-7 at K = 4052).
 //
 // Epilogue: with PROMOTE 8 warps (two per TMEM lane quadrant; their accumulators take the
 // registers), else 16, whose activations hide one another's latencies. A thread owns a row
@@ -55,7 +57,8 @@ constexpr int kRows = kLinearTileM / 2;  // of a tile per CTA
 constexpr int BN = kLinearTileN;
 constexpr int kCols = BN / 2;            // columns of B per CTA
 constexpr int kK = 64;                   // K per stage: one 128-byte swizzled row of bf16
-constexpr int kSegment = 8;              // K blocks between two takings (PROMOTE); planes: 4
+constexpr int kSegment = 8;              // K blocks between two takings (PROMOTE)
+constexpr int kPlaneSegment = 4;         // the same where operands have planes
 constexpr uint32_t kABytes = kRows * kK * 2;
 constexpr uint32_t kMnBlock = 64 * kK * 2;   // 64 MN x 64 K of an MN-major operand
 
@@ -400,8 +403,11 @@ __global__ void __launch_bounds__(Tile<AP, PROMOTE>::kThreads, 1) linear_tc_kern
   const int mt = (M + 2 * kRows - 1) / (2 * kRows);
   const int nt = (N + BN - 1) / BN;
   const int pair = blockIdx.x >> 1;
-  // Segments of a piece of k K blocks.
-  const auto segment = [](int k) { return PROMOTE ? (AP > 1 ? kSegment / 2 : kSegment) : k; };
+  // K blocks of a segment of a piece of k, and of the producer's walk, whose order only
+  // matters with planes.
+  constexpr int kGroup = AP > 1 ? kPlaneSegment : kSegment;
+  static_assert(AP == 1 || PROMOTE, "planes: fp32 outputs");
+  const auto segment = [](int k) { return PROMOTE ? kGroup : k; };
   let_next_in();
 
   if (threadIdx.x == 0) {
@@ -443,36 +449,38 @@ __global__ void __launch_bounds__(Tile<AP, PROMOTE>::kThreads, 1) linear_tc_kern
         const TileAt mn = tile_at(pc.tile, mt, nt);
         const int m0 = mn.m * (2 * kRows) + rank * kRows;
         const int n0 = mn.n * BN + rank * kCols;
-        for (int kb = pc.kb0; kb < pc.kb1 && ok; ++kb) {
-          const int k0 = kb * kK;
-          for (int i = 0; i < nsteps; ++i) {
-          const int what = AP > 1 ? step_planes(steps, i) : 0x1000;
-          const int count = AP > 1 ? what >> 12 : 1, pb = (what >> 8) & 15;
-          if (!mbar_wait(&empty[s], ph ^ 1, status, abort)) { ok = false; break; }
-          uint8_t* a = stages + s * T::kStage;
-          uint8_t* b = a + AP * kABytes;
-          const uint32_t bar = leader_addr(&full[s]);
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (count * kABytes + T::kBBytes));
+        for (int g0 = pc.kb0; g0 < pc.kb1 && ok; g0 += kGroup) {
+          const int blocks = min(kGroup, pc.kb1 - g0);
+          for (int i = 0; i < blocks * nsteps; ++i) {
+            const int step = i / blocks;
+            const int k0 = (g0 + i - step * blocks) * kK;
+            const int what = AP > 1 ? step_planes(steps, step) : 0x1000;
+            const int count = AP > 1 ? what >> 12 : 1, pb = (what >> 8) & 15;
+            if (!mbar_wait(&empty[s], ph ^ 1, status, abort)) { ok = false; break; }
+            uint8_t* a = stages + s * T::kStage;
+            uint8_t* b = a + AP * kABytes;
+            const uint32_t bar = leader_addr(&full[s]);
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (count * kABytes + T::kBBytes));
 #pragma unroll
-          for (int p = 0; p < AP; ++p) {
-            if (p >= count) break;
-            const int pa = (what >> (4 * p)) & 15;
-            if (A_MN) {
-              tma_load_3d_pair(a + p * kABytes, &tm_a, bar, m0, k0, pa);
-              tma_load_3d_pair(a + p * kABytes + kMnBlock, &tm_a, bar, m0 + 64, k0, pa);
-            } else {
-              tma_load_3d_pair(a + p * kABytes, &tm_a, bar, k0, m0, pa);
+            for (int p = 0; p < AP; ++p) {
+              if (p >= count) break;
+              const int pa = (what >> (4 * p)) & 15;
+              if (A_MN) {
+                tma_load_3d_pair(a + p * kABytes, &tm_a, bar, m0, k0, pa);
+                tma_load_3d_pair(a + p * kABytes + kMnBlock, &tm_a, bar, m0 + 64, k0, pa);
+              } else {
+                tma_load_3d_pair(a + p * kABytes, &tm_a, bar, k0, m0, pa);
+              }
             }
-          }
-          if (B_MN) {
+            if (B_MN) {
 #pragma unroll
-            for (int blk = 0; blk < kCols / 64; ++blk)
-              tma_load_3d_pair(b + blk * kMnBlock, &tm_b, bar, n0 + 64 * blk, k0, pb);
-          } else {
-            tma_load_3d_pair(b, &tm_b, bar, k0, n0, pb);
-          }
-          ++issued;
-          if (++s == T::kStages) { s = 0; ph ^= 1; }
+              for (int blk = 0; blk < kCols / 64; ++blk)
+                tma_load_3d_pair(b + blk * kMnBlock, &tm_b, bar, n0 + 64 * blk, k0, pb);
+            } else {
+              tma_load_3d_pair(b, &tm_b, bar, k0, n0, pb);
+            }
+            ++issued;
+            if (++s == T::kStages) { s = 0; ph ^= 1; }
           }
         }
       }
@@ -504,16 +512,14 @@ __global__ void __launch_bounds__(Tile<AP, PROMOTE>::kThreads, 1) linear_tc_kern
       while (ok && work.next(&pc)) {
         const int kblocks = pc.kb1 - pc.kb0, seg = segment(kblocks);
         for (int k = 0; k < kblocks && ok; k += seg, ++it) {
-          const int here = min(seg, kblocks - k) * nsteps;
+          const int blocks = min(seg, kblocks - k);   // with planes at most kGroup
           const int buf = it & 1;
           const uint32_t tph = (it >> 1) & 1;
           if (!mbar_wait(&tempty[buf], tph ^ 1, status, abort)) { ok = false; break; }
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + buf * BN;
-          int step = 0;
-          for (int i = 0; i < here; ++i) {
-            const int count = AP > 1 ? step_planes(steps, step) >> 12 : 1;
-            if (++step == nsteps) step = 0;
+          for (int i = 0; i < blocks * nsteps; ++i) {
+            const int count = AP > 1 ? step_planes(steps, i / blocks) >> 12 : 1;
             if (!mbar_wait(&full[s], ph, status, abort)) { ok = false; break; }
             tc_fence_after();
             const uint32_t a = smem_addr(stages + s * T::kStage);

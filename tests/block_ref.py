@@ -126,12 +126,15 @@ def adamw(t, hyper, index):
     h = mix32((i // 2) ^ key)
     b = torch.where(i % 2 == 0, h & 0xffff, h >> 16).double()
     ulp = torch.ldexp(torch.ones_like(b), (torch.frexp(q.double())[1] - 1).clamp(min=-6) - 3)
-    raw = q.double() + ulp * (b - 32767.5) / 65536
-    near = ((raw / ulp).round() * ulp).clamp(min=2.0 ** -9)
-    out["v"] = torch.where(q > 0, near.float(), q).to(torch.float8_e4m3fn)
+    near = (q + (ulp * (b - 32767.5) / 65536).float()).clamp(2.0 ** -9, 448.0)
+    out["v"] = torch.where(q > 0, near, q).to(torch.float8_e4m3fn)
     # The kernel's root is good to 2^-22: 2^-18 of a code at most (16 steps an octave), so a
-    # value this near to the middle of two codes may go to either.
-    out["v_edge"] = ((raw / ulp - (raw / ulp).floor() - 0.5).abs() < 2.0 ** -16) & (q > 0)
+    # value this near to the middle of two codes may go to either, and one this near to a power
+    # of two may have the dither of the other side (half or twice as wide).
+    at = torch.ldexp(torch.ones_like(b), (torch.frexp(near.double())[1] - 1).clamp(min=-6) - 3)
+    part = near.double() / at
+    power = ((torch.frexp(q.double())[0] * 2 - 1.5).abs() - 0.5).abs() < 2.0 ** -20
+    out["v_edge"] = (((part - part.floor() - 0.5).abs() < 2.0 ** -16) | power) & (q > 0)
     return out
 
 

@@ -170,16 +170,20 @@ def test_non_finite_gradients_stay_in_their_block(bits):
 
 def test_a_moment_that_is_a_code_stays_that_code():
     """With beta2 = 0 the new r is |g|: a gradient of codes times a power of two comes back as
-    it is whatever the dither, powers of two among them."""
+    it is whatever the dither, but for powers of two, which may go one code down."""
     import product_key_memory_b200 as P
-    codes = torch.arange(0, 127, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
-    g = codes.float().repeat(40)[:256 * 19] * 2.0 ** -12
+    codes = torch.arange(0, 127, dtype=torch.uint8, device="cuda")
+    two = ((codes & 7) == 0) & (codes > 8)        # the codes below lie half as far apart
+    two = two.repeat(40)[:256 * 19]
+    codes = codes.repeat(40)[:256 * 19]
+    g = codes.view(torch.float8_e4m3fn).float() * 2.0 ** -12
     t = dict(param=torch.zeros_like(g), grad=g, **P.alloc_adamw_state(g, 8))
     lst = P.make_adamw_tensors([t])
     for step in range(1, 9):
         P.pkm_adamw_step(lst, lr=0.0, step=step, betas=(0.0, 0.0), seed=step)
-        for k in ("m", "v"):
-            assert torch.equal(t[k].float() * t[k + "_scale"].repeat_interleave(256), g)
+        m, v = (t[k].float() * t[k + "_scale"].repeat_interleave(256) for k in ("m", "v"))
+        assert torch.equal(m, g) and torch.equal(v[~two], g[~two])
+        assert bool(((v[two] == g[two]) | (v[two] == g[two] * (15 / 16))).all())
 
 
 def test_a_moment_without_gradients_decays_at_its_rate():
@@ -199,9 +203,12 @@ def test_a_moment_without_gradients_decays_at_its_rate():
     r1 = (t["v"].float() * t["v_scale"].repeat_interleave(256)).double()
     # Each element's r falls by 0.999^(200/2) = 0.9048 on average. The dither's noise per step is
     # at most sqrt(5e-4 * step size 1/8) of r, over 200 steps below 12 % of an element and
-    # below 0.12 / 2^8 of the mean over 2^16: five of those and the 1e-3 of drift of r^2.
+    # below 0.12 / 2^8 of the mean over 2^16: five of those and the 1e-3 of drift of r^2. An
+    # element that passes a power of two on its way (log2(1 / 0.9048) = 14.4 % of them) may
+    # be one code, 1/16, further down there.
     ratio = (r1.sum() / r0.sum()).item()
-    assert abs(ratio - 0.999 ** 100) < 5 * 0.12 / 256 + 1e-3
+    noise = 5 * 0.12 / 256 + 1e-3
+    assert -0.144 / 16 - noise < ratio - 0.999 ** 100 < noise
 
 
 def test_deterministic_and_seeded():
