@@ -43,12 +43,18 @@ template <> struct Raw<BF16, 8> {
   __device__ __forceinline__ void load(const void* p, int64_t i) {
     a = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i));
   }
+  __device__ __forceinline__ void load_again(const void* p, int64_t i) {
+    a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+  }
   __device__ __forceinline__ void get(float* f) const { Vec<uint16_t>::widen(a, f); }
 };
 template <> struct Raw<F32, 4> {
   float4 a;
   __device__ __forceinline__ void load(const void* p, int64_t i) {
     a = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
+  }
+  __device__ __forceinline__ void load_again(const void* p, int64_t i) {
+    a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
   }
   __device__ __forceinline__ void get(float* f) const {
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
@@ -69,12 +75,18 @@ template <> struct Raw<F32, 1> {
   __device__ __forceinline__ void load(const void* p, int64_t i) {
     a = __ldcs(static_cast<const float*>(p) + i);
   }
+  __device__ __forceinline__ void load_again(const void* p, int64_t i) {
+    a = static_cast<const float*>(p)[i];
+  }
   __device__ __forceinline__ void get(float* f) const { f[0] = a; }
 };
 template <> struct Raw<BF16, 1> {
   uint16_t a;
   __device__ __forceinline__ void load(const void* p, int64_t i) {
     a = __ldcs(static_cast<const unsigned short*>(p) + i);
+  }
+  __device__ __forceinline__ void load_again(const void* p, int64_t i) {
+    a = static_cast<const uint16_t*>(p)[i];
   }
   __device__ __forceinline__ void get(float* f) const {
     f[0] = __uint_as_float(static_cast<uint32_t>(a) << 16);

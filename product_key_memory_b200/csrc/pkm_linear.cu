@@ -3,6 +3,8 @@
 // product's tiles are shared out.
 #include "pkm_linear.h"
 
+#include <type_traits>
+
 #include "pkm_block.h"
 #include "pkm_linear_epi.cuh"
 #include "pkm_tc.h"
@@ -23,58 +25,108 @@ __device__ __forceinline__ void clear_status(int* status) {
 }
 
 // ---------------------------------------------------------------- small batches
-// One warp per output column: the lanes split the W row (read once, 4 accesses in flight),
-// x comes from L1/L2, the lanes' sums are added by a tree. Bound by reading W.
+constexpr int kSmallCols = 4;
+
+// Sums of NV values over a warp, NV a power of two up to 32: each exchange halves the values a
+// lane keeps. Returns the sum of value lane / (32 / NV).
+template <int NV>
+__device__ __forceinline__ float warp_sums(float* v, int lane) {
+  int o = 16;
+#pragma unroll
+  for (int n = NV / 2; n > 0; n /= 2, o /= 2) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+  float s = v[0];
+  for (; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
+// A warp has four columns, so that a piece of x (from L1 or L2) serves four rows of W, and one
+// of `slices` shares of K; the lanes' sums are added by a tree, the slices' in order. With few
+// rows W's bytes bound it (16384 x 16384 bf16, 1 row: 86 us, 6.2 TB/s), with 8 the reading of
+// x, M / 4 times W's bytes from L1 (166 us; 2 columns a warp 169, and slower with fewer
+// rows). 1024 -> 4096 bf16, 1 row: 3.2 us; 5590 -> 2972 fp32, 4 rows: 16 us.
 template <typename E, int V, int M>
 __global__ void __launch_bounds__(256) linear_small_kernel(const void* x, const void* W, int N,
-                                                           int K, const LinearEpilogue epi,
+                                                           int K, int slices,
+                                                           const LinearEpilogue epi,
                                                            int* status) {
+  constexpr int C = kSmallCols;
+  constexpr int NV = C * M <= 4 ? 4 : C * M <= 8 ? 8 : C * M <= 16 ? 16 : 32;
+  // Accesses of a W row in flight. More rows hold more of x in registers; of single elements,
+  // four times as many cost one row's sectors their place in L1 (17 -> 38 us at 5591 -> 2972).
+  constexpr int kDepth = V == 1 ? (M <= 2 ? 4 : 8) : M <= 2 ? 2 : 1;
+  __shared__ float sums[8][NV];
   let_next_in();
   wait_for_previous();
   clear_status(status);
-  const int lane = threadIdx.x & 31;
-  const int col = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (col >= N) return;
-  const int64_t base = static_cast<int64_t>(col) * K;
-  float acc[M] = {};
-  constexpr int kDepth = V == 1 ? 16 : 4;
-  for (int k0 = lane * V; k0 < K; k0 += 32 * V * kDepth) {
-    Raw<E, V> w[kDepth];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int groups = 8 / slices;
+  const int col0 = (blockIdx.x * groups + warp / slices) * C;
+  float acc[NV] = {};   // [m][c]
+  constexpr int stride = 32 * V;
+  const int share = (K + stride * slices - 1) / (stride * slices) * stride;
+  int k0 = warp % slices * share;
+  const int k1 = min(K, k0 + share);
+  k0 += lane * V;
+  const auto pieces = [&](auto depth) {
+    constexpr int kDepth = decltype(depth)::value;
+    Raw<E, V> w[kDepth][C];
 #pragma unroll
     for (int u = 0; u < kDepth; ++u)
-      if (k0 + u * 32 * V < K) w[u].load(W, base + k0 + u * 32 * V);
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        w[u][c].load(W, static_cast<int64_t>(min(col0 + c, N - 1)) * K + k0 + u * stride);
 #pragma unroll
     for (int u = 0; u < kDepth; ++u) {
-      const int k = k0 + u * 32 * V;
-      if (k >= K) break;
-      float wf[V];
-      w[u].get(wf);
+      Raw<E, V> xr[M];
+#pragma unroll
+      for (int m = 0; m < M; ++m) xr[m].load_again(x, static_cast<int64_t>(m) * K + k0 + u * stride);
+      float wf[C][V];
+#pragma unroll
+      for (int c = 0; c < C; ++c) w[u][c].get(wf[c]);
 #pragma unroll
       for (int m = 0; m < M; ++m) {
-        Raw<E, V> xr;
         float xf[V];
-        xr.load(x, static_cast<int64_t>(m) * K + k);
-        xr.get(xf);
+        xr[m].get(xf);
 #pragma unroll
-        for (int v = 0; v < V; ++v) acc[m] = fmaf(wf[v], xf[v], acc[m]);
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[m * C + c] = fmaf(wf[c][v], xf[v], acc[m * C + c]);
       }
     }
-  }
-  float mine = 0.f;
-#pragma unroll
-  for (int m = 0; m < M; ++m) {
-    const float s = warp_sum(acc[m]);
-    if (lane == m) mine = s;
-  }
-  if (lane < M) linear_store1(epi, static_cast<int64_t>(lane) * N + col, col, mine);
+    k0 += stride * kDepth;
+  };
+  while (k0 + (kDepth - 1) * stride < k1) pieces(std::integral_constant<int, kDepth>());
+  while (k0 < k1) pieces(std::integral_constant<int, 1>());
+  __syncwarp();
+  const float s = warp_sums<NV>(acc, lane);
+  if (lane % (32 / NV) == 0) sums[warp][lane / (32 / NV)] = s;
+  __syncthreads();
+  const int g = threadIdx.x / NV, i = threadIdx.x % NV;
+  const int col = (blockIdx.x * groups + g) * C + i % C;
+  if (g >= groups || i >= C * M || col >= N) return;
+  float total = 0.f;
+  for (int j = 0; j < slices; ++j) total += sums[g * slices + j][i];
+  linear_store1(epi, static_cast<int64_t>(i / C) * N + col, col, total);
 }
 
 template <typename E, int V>
 cudaError_t run_small(int M, const void* x, const void* W, int N, int K,
                       const LinearEpilogue& epi, int* status, cudaStream_t st) {
-  const unsigned grid = static_cast<unsigned>((N + 7) / 8);
+  // K is shared out until there are 16 warps an SM or a slice has one access a row.
+  const int64_t warps = (N + kSmallCols - 1) / kSmallCols;
+  int slices = 1;
+  while (slices < 8 && slices * 32 * V < K && warps * slices < 16 * sm_count()) slices *= 2;
+  const int per = 8 / slices * kSmallCols;
+  const unsigned grid = static_cast<unsigned>((N + per - 1) / per);
   const auto run = [&](auto* kernel) {
-    return launch_after(kernel, grid, 256, 0, 1, st, x, W, N, K, epi, status);
+    return launch_after(kernel, grid, 256, 0, 1, st, x, W, N, K, slices, epi, status);
   };
   switch (M) {
     case 1: return run(linear_small_kernel<E, V, 1>);
@@ -396,9 +448,9 @@ cudaError_t launch_linear_forward(const LinearArgs& a, const void* x, const void
   if (linear_small(a)) {
     ++*launches;
     const int M = static_cast<int>(a.M);
-    const bool vec = a.K % 8 == 0;
+    const bool vec = a.K % (a.dtype == PKM_F32 ? 4 : 8) == 0;   // rows of whole 16 bytes
     if (a.dtype == PKM_F32)
-      return vec ? run_small<F32, 8>(M, x, W, a.N, a.K, epi, first, st)
+      return vec ? run_small<F32, 4>(M, x, W, a.N, a.K, epi, first, st)
                  : run_small<F32, 1>(M, x, W, a.N, a.K, epi, first, st);
     return vec ? run_small<BF16, 8>(M, x, W, a.N, a.K, epi, first, st)
                : run_small<BF16, 1>(M, x, W, a.N, a.K, epi, first, st);
