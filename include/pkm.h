@@ -392,9 +392,9 @@ int pkm_linear_forward(const pkm_linear_shape* s, const void* x, const void* W, 
  * each overwritten and each may be NULL (not computed). The residual's gradient is grad_y.
  *   x, W as in the forward; grad_y [M][N] dtype; pre [M][N] dtype as the forward wrote it
  *   (not read, may be NULL, without an activation)
- * d is an fp32 value. In fp32 layers it enters the products as three bf16 planes, in bf16
- * layers with an activation as two (hi + lo, within 2^-17 of d), and as hi alone in a bf16
- * grad_x, whose own rounding is as large. Column sums add in a fixed order; all results are
+ * d is an fp32 value. With an activation and in fp32 layers it enters the products as three
+ * bf16 planes whose sum is d to 2^-24; in a bf16 grad_x as one, rounded to bf16, which is no
+ * more than grad_x's own rounding. Column sums add in a fixed order; all results are
  * bit-for-bit the same on every run.
  * workspace: pkm_linear_workspace_size(s, 1) bytes, 256-byte aligned, status word as above.
  */
@@ -436,8 +436,8 @@ typedef struct {
  * One AdamW step (Loshchilov and Hutter, decoupled weight decay) over a list of tensors:
  *   g = grad grad_scale,  m <- beta1 m + (1 - beta1) g,  v <- beta2 v + (1 - beta2) g^2
  *   p <- p (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
- * in fp32, with lr = hyper.lr lr_scale (square roots and quotients to 2^-22). The moments that move p are the new ones before
- * they are rounded to 8 bits.
+ * in fp32, with lr = hyper.lr lr_scale (square roots and quotients to 2^-22). The moments
+ * that move p are the new ones before they are rounded to 8 bits.
  * 8-bit states (after the block-wise states of Dettmers et al., "8-bit Optimizers via
  * Block-wise Quantization"): m and r = sqrt(v) as fp8 e4m3 codes, each block of 256
  * elements (counted from the tensor's start) with its scale s = the smallest power of two,

@@ -326,17 +326,19 @@ cudaError_t run_slope(int planes, const void* gy, const void* pre, int act, uint
   const int64_t ld = pad8(cols);
   auto* kernel = planes == 0   ? linear_slope_kernel<E, V, 0>
                  : planes == 1 ? linear_slope_kernel<E, V, 1>
-                 : planes == 2 ? linear_slope_kernel<E, V, 2>
                                : linear_slope_kernel<E, V, 3>;
   return launch_after(kernel, grid, 256, 0, 1, st, gy, pre, act, dst, part, rows, cols, ld, status);
 }
 
 // ------------------------------------------------------------------- host side
 // How a product is shared out over the 74 pairs of CTAs of a B200 (fixed, because the
-// workspace's size depends on it). Fewer tiles than pairs: cut along K for more pairs where
-// that takes less time, counted in K steps of a tile (0.3 us): the longest range, the
-// join kernel (12), and each pair's part, written and read at about 5 TB/s (256 rows: a third).
-// 777 x 4096 -> 1024 takes 20.8 us cut and 28.5 whole, 2048 x 2048 -> 2048 27 and 19.7.
+// workspace's size depends on it), counted in K steps of a tile (0.3 us). More tiles than
+// pairs: whole rounds, and the tiles of the last one cut along K over all pairs where that
+// saves more than the parts cost (below). Fewer: cut for more pairs where that takes less
+// time: the longest range, the join kernel (12), and each pair's part, written and read at
+// about 5 TB/s (256 rows: a third). 777 x 4096 -> 1024 takes 20.8 us cut and 28.5 whole, 2048 x
+// 2048 -> 2048 27 and 19.7; grad_W of 4096 x 1600 -> 6400 gelu, 175 tiles, 265 us with the last
+// 27 cut and 305 whole.
 constexpr int kPairs = 74;
 constexpr int kMinSteps = 8;      // of a range
 
@@ -347,9 +349,18 @@ LinearWork share_out(int64_t M, int64_t N, int64_t K, int products) {
   const int64_t steps = static_cast<int64_t>(kblocks) * products;   // of one tile
   LinearWork best{static_cast<int>(tiles < kPairs ? tiles : kPairs), static_cast<int>(tiles), 0,
                   kblocks};
+  if (tiles > kPairs) {
+    const int rest = static_cast<int>(tiles % kPairs);
+    const double idle = static_cast<double>(steps) * (kPairs - rest) / kPairs;
+    if (rest && rest * steps >= kPairs * kMinSteps && idle > 12 + kPairs / 3.0) {
+      best.cut = rest;
+      best.whole -= rest;
+    }
+    return best;
+  }
   double least = static_cast<double>(steps);
   const double rows = M < kLinearTileM ? static_cast<double>(M) / kLinearTileM : 1.0;
-  for (int64_t ways = 2; tiles < kPairs && ways <= 32; ++ways) {
+  for (int64_t ways = 2; ways <= 32; ++ways) {
     const int64_t pairs = ways * tiles < kPairs ? ways * tiles : kPairs;
     // No range is empty, or too short to be worth it.
     if (pairs > tiles * kblocks || pairs * kMinSteps > tiles * steps) break;
@@ -365,10 +376,14 @@ LinearWork share_out(int64_t M, int64_t N, int64_t K, int products) {
 
 // The products of a's and b's planes, p + q below the larger plane count, smallest first.
 LinearSteps plane_steps(int a, int b) {
-  // (planes of A, plane of B): {0} 2, {1, 0} 1, {2, 1} 0, {0} 0.
-  if (a == 3 && b == 3) return {0x1000'2012'2101'1200ull, 4, 6};
-  if (a == 2) return {0x2001, 1, 2};                                    // {1, 0} 0
-  return {0x1000, 1, 1};
+  const auto step = [](int pb, int count, int p0, int p1, int p2) {
+    return static_cast<uint64_t>(p0 | p1 << 4 | p2 << 8 | pb << 12 | count << 14);
+  };
+  if (a == 3 && b == 3)
+    return {step(2, 1, 0, 0, 0) | step(1, 2, 1, 0, 0) << 16 | step(0, 2, 2, 1, 0) << 32 |
+                step(0, 1, 0, 0, 0) << 48, 4, 6};
+  if (a == 3) return {step(0, 3, 2, 1, 0), 1, 3};
+  return {step(0, 1, 0, 0, 0), 1, 1};
 }
 
 // Number of planes of an operand of the layer's type; in place (0 bytes) for bf16 rows of
@@ -386,8 +401,7 @@ size_t part_bytes(const LinearWork& w) {
 
 // The backward's d: planes written (0: grad_y itself is the operand).
 int slope_planes(const LinearArgs& a) {
-  if (a.dtype == PKM_F32) return 3;
-  if (a.act != PKM_ACT_NONE) return 2;
+  if (a.dtype == PKM_F32 || a.act != PKM_ACT_NONE) return 3;
   return a.N % 8 == 0 ? 0 : 1;
 }
 
@@ -413,7 +427,7 @@ Layout layout(const LinearArgs& a, bool backward) {
   } else {
     const int d = slope_planes(a);
     // grad_x in bf16: d's rounding to bf16 is no larger than grad_x's own, one plane will do.
-    l.gx_p = plane_steps(d == 2 && a.out_dtype == PKM_BF16 ? 1 : (d ? d : 1), in);
+    l.gx_p = plane_steps(in == 1 && a.out_dtype == PKM_BF16 ? 1 : (d ? d : 1), in);
     l.gw_p = plane_steps(d ? d : 1, in);
     l.gx = share_out(a.M, a.K, a.N, l.gx_p.products);
     l.gw = share_out(a.N, a.K, a.M, l.gw_p.products);
@@ -489,7 +503,8 @@ cudaError_t launch_linear_backward(const LinearArgs& a, const void* x, const voi
   const bool want_d = grad_x || grad_W;
   if (grad_bias || (want_d && dp > 0)) {
     float* part = grad_bias ? reinterpret_cast<float*>(ws + l.bias) : nullptr;
-    const int planes = want_d ? dp : 0;
+    const bool one = dp > 1 && !grad_W && l.gx_p.products == 1;
+    const int planes = !want_d ? 0 : one ? 1 : dp;
     const bool vec = a.N % 8 == 0;
     if (a.dtype == PKM_F32)
       e = vec ? run_slope<F32, 8>(planes, grad_y, pre, a.act, d, part, a.M, a.N, first, st)

@@ -69,8 +69,8 @@ struct LinearWork {
   }
 };
 
-// The plane products of one K block: step i (16 bits from bit 16 i) multiplies `count` planes of
-// A (bits 12..15), nibbles 0.. in this order, with one plane of B (nibble 2).
+// The plane products of one K block: step i (16 bits from bit 16 i) multiplies up to three planes
+// of A (nibbles 0..2 in this order, their number in bits 14..15) with one of B (bits 12..13).
 struct LinearSteps {
   uint64_t packed;
   int count, products;

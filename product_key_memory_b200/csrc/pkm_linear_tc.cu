@@ -10,8 +10,9 @@
 // majorness. bf16 operands are one plane. An fp32 operand arrives as bf16 planes
 // hi, mid, lo whose sum is the value to 2^-24, and the products whose size is above 2^-24
 // are added in one fp32 accumulator. A step of the K loop is one K block of one plane of B
-// and of up to AP planes of A, each multiplied with it: a B tile is loaded once for two
-// products.
+// and of up to three planes of A, each multiplied with it: a B tile is loaded once for
+// them. With planes a stage is one tile of one operand (10 of 16 KiB in a CTA; stages of a
+// whole step, 3 of them, did not hide L2's latency).
 //
 // A tile is 256 x 256 outputs of a pair of CTAs that shares each MMA (cta_group::2): every
 // CTA loads half of A's rows and half of B's columns. What bounds the product is the
@@ -62,9 +63,11 @@ constexpr int kPlaneSegment = 4;         // the same where operands have planes
 constexpr uint32_t kABytes = kRows * kK * 2;
 constexpr uint32_t kMnBlock = 64 * kK * 2;   // 64 MN x 64 K of an MN-major operand
 
-template <int AP, bool PROMOTE> struct Tile {
+template <bool PLANES, bool PROMOTE> struct Tile {
   static constexpr uint32_t kBBytes = kCols * kK * 2;
-  static constexpr uint32_t kStage = AP * kABytes + kBBytes;
+  // A K block of both operands, or of one plane of either.
+  static constexpr uint32_t kStage = PLANES ? kABytes : kABytes + kBBytes;
+  static_assert(kABytes == kBBytes, "one size of stage");
   static constexpr int kStages = 163840 / kStage;            // up to 160 KiB of stages
   // Epilogue warps: each takes kWide columns of its quadrant's rows.
   static constexpr int kWide = PROMOTE ? BN / 2 : BN / 4;
@@ -379,14 +382,14 @@ __device__ __forceinline__ void store_part(const CUtensorMap* tm_part, Outputs& 
   o.part_before = true;
 }
 
-template <bool A_MN, bool B_MN, int AP, bool PROMOTE>
-__global__ void __launch_bounds__(Tile<AP, PROMOTE>::kThreads, 1) linear_tc_kernel(
+template <bool A_MN, bool B_MN, bool PLANES, bool PROMOTE>
+__global__ void __launch_bounds__(Tile<PLANES, PROMOTE>::kThreads, 1) linear_tc_kernel(
     const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
     const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_pre,
     const __grid_constant__ CUtensorMap tm_part, int M, int N, const uint64_t steps,
     const int nsteps, const LinearWork plan, int use_tma, const LinearEpilogue epi,
     int* status, int clear) {
-  using T = Tile<AP, PROMOTE>;
+  using T = Tile<PLANES, PROMOTE>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = align1024(smem_raw);
   uint8_t* staging = stages + T::kStages * T::kStage;
@@ -405,8 +408,8 @@ __global__ void __launch_bounds__(Tile<AP, PROMOTE>::kThreads, 1) linear_tc_kern
   const int pair = blockIdx.x >> 1;
   // K blocks of a segment of a piece of k, and of the producer's walk, whose order only
   // matters with planes.
-  constexpr int kGroup = AP > 1 ? kPlaneSegment : kSegment;
-  static_assert(AP == 1 || PROMOTE, "planes: fp32 outputs");
+  constexpr int kGroup = PLANES ? kPlaneSegment : kSegment;
+  static_assert(!PLANES || PROMOTE, "planes: fp32 outputs");
   const auto segment = [](int k) { return PROMOTE ? kGroup : k; };
   let_next_in();
 
@@ -454,33 +457,37 @@ __global__ void __launch_bounds__(Tile<AP, PROMOTE>::kThreads, 1) linear_tc_kern
           for (int i = 0; i < blocks * nsteps; ++i) {
             const int step = i / blocks;
             const int k0 = (g0 + i - step * blocks) * kK;
-            const int what = AP > 1 ? step_planes(steps, step) : 0x1000;
-            const int count = AP > 1 ? what >> 12 : 1, pb = (what >> 8) & 15;
-            if (!mbar_wait(&empty[s], ph ^ 1, status, abort)) { ok = false; break; }
-            uint8_t* a = stages + s * T::kStage;
-            uint8_t* b = a + AP * kABytes;
-            const uint32_t bar = leader_addr(&full[s]);
-            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (count * kABytes + T::kBBytes));
-#pragma unroll
-            for (int p = 0; p < AP; ++p) {
-              if (p >= count) break;
-              const int pa = (what >> (4 * p)) & 15;
-              if (A_MN) {
-                tma_load_3d_pair(a + p * kABytes, &tm_a, bar, m0, k0, pa);
-                tma_load_3d_pair(a + p * kABytes + kMnBlock, &tm_a, bar, m0 + 64, k0, pa);
-              } else {
-                tma_load_3d_pair(a + p * kABytes, &tm_a, bar, k0, m0, pa);
+            const int what = PLANES ? step_planes(steps, step) : 1 << 14;
+            // B's stage (without planes A's too), then A's planes.
+            for (int p = PLANES ? -1 : 0; p < what >> 14; ++p) {
+              if (!mbar_wait(&empty[s], ph ^ 1, status, abort)) { ok = false; break; }
+              uint8_t* to = stages + s * T::kStage;
+              const uint32_t bar = leader_addr(&full[s]);
+              if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * T::kStage);
+              if (p >= 0) {
+                const int pa = (what >> (4 * p)) & 15;
+                if (A_MN) {
+                  tma_load_3d_pair(to, &tm_a, bar, m0, k0, pa);
+                  tma_load_3d_pair(to + kMnBlock, &tm_a, bar, m0 + 64, k0, pa);
+                } else {
+                  tma_load_3d_pair(to, &tm_a, bar, k0, m0, pa);
+                }
               }
-            }
-            if (B_MN) {
+              if (!PLANES || p < 0) {
+                const int pb = (what >> 12) & 3;
+                uint8_t* b = PLANES ? to : to + kABytes;
+                if (B_MN) {
 #pragma unroll
-              for (int blk = 0; blk < kCols / 64; ++blk)
-                tma_load_3d_pair(b + blk * kMnBlock, &tm_b, bar, n0 + 64 * blk, k0, pb);
-            } else {
-              tma_load_3d_pair(b, &tm_b, bar, k0, n0, pb);
+                  for (int blk = 0; blk < kCols / 64; ++blk)
+                    tma_load_3d_pair(b + blk * kMnBlock, &tm_b, bar, n0 + 64 * blk, k0, pb);
+                } else {
+                  tma_load_3d_pair(b, &tm_b, bar, k0, n0, pb);
+                }
+              }
+              ++issued;
+              if (++s == T::kStages) { s = 0; ph ^= 1; }
             }
-            ++issued;
-            if (++s == T::kStages) { s = 0; ph ^= 1; }
+            if (!ok) break;
           }
         }
       }
@@ -519,25 +526,31 @@ __global__ void __launch_bounds__(Tile<AP, PROMOTE>::kThreads, 1) linear_tc_kern
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + buf * BN;
           for (int i = 0; i < blocks * nsteps; ++i) {
-            const int count = AP > 1 ? step_planes(steps, i / blocks) >> 12 : 1;
-            if (!mbar_wait(&full[s], ph, status, abort)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t a = smem_addr(stages + s * T::kStage);
-            const uint32_t b = a + AP * kABytes;
-#pragma unroll
-            for (int p = 0; p < AP; ++p) {
-              if (p >= count) break;
+            const int count = PLANES ? step_planes(steps, i / blocks) >> 14 : 1;
+            uint32_t b = 0, b_stage = 0;
+            if (PLANES) {
+              if (!mbar_wait(&full[s], ph, status, abort)) { ok = false; break; }
+              b = smem_addr(stages + s * T::kStage);
+              b_stage = s;
+              if (++s == T::kStages) { s = 0; ph ^= 1; }
+            }
+            for (int p = 0; p < count; ++p) {
+              if (!mbar_wait(&full[s], ph, status, abort)) { ok = false; break; }
+              tc_fence_after();
+              const uint32_t a = smem_addr(stages + s * T::kStage);
+              if (!PLANES) b = a + kABytes;
 #pragma unroll
               for (int j = 0; j < kK / 16; ++j) {
                 // 16 K = two 8-row atoms of an MN-major tile, 32 bytes of a K-major row.
-                const uint32_t ap = a + p * kABytes;
-                const uint64_t ad = A_MN ? mn_desc(ap + j * 2048) : sw128_desc(ap, j * 32);
+                const uint64_t ad = A_MN ? mn_desc(a + j * 2048) : sw128_desc(a, j * 32);
                 const uint64_t bd = B_MN ? mn_desc(b + j * 2048) : sw128_desc(b, j * 32);
                 mma_bf16_pair(d_tmem, ad, bd, idesc, (i != 0 || p != 0 || j != 0) ? 1u : 0u);
               }
+              mma_commit_pair(&empty[s]);
+              if (++s == T::kStages) { s = 0; ph ^= 1; }
             }
-            mma_commit_pair(&empty[s]);
-            if (++s == T::kStages) { s = 0; ph ^= 1; }
+            if (!ok) break;
+            if (PLANES) mma_commit_pair(&empty[b_stage]);
           }
           if (ok) mma_commit_pair(&tfull[buf]);
         }
@@ -701,9 +714,9 @@ bool output_map(CUtensorMap* m, const void* p, bool f32, int64_t cols, int64_t r
                   f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 }
 
-template <bool A_MN, bool B_MN, int AP, bool PROMOTE>
+template <bool A_MN, bool B_MN, bool PLANES, bool PROMOTE>
 cudaError_t run(const LinearGemm& g, int* launches, cudaStream_t st) {
-  using T = Tile<AP, PROMOTE>;
+  using T = Tile<PLANES, PROMOTE>;
   CUtensorMap tm_a, tm_b;
   // K-major: [planes][rows][K]; MN-major: [planes][K][columns]; ld elements a row.
   const cuuint64_t al = static_cast<cuuint64_t>(g.lda) * 2, bl = static_cast<cuuint64_t>(g.ldb) * 2;
@@ -725,7 +738,7 @@ cudaError_t run(const LinearGemm& g, int* launches, cudaStream_t st) {
       (tma && e.pre && !output_map(&tm_pre, e.pre, e.pre_f32, g.N, g.M, 1, box)) ||
       (g.part && !output_map(&tm_part, g.part, true, BN, 2 * kRows, 2 * g.work.pairs)))
     return cudaErrorInvalidValue;
-  auto* kernel = linear_tc_kernel<A_MN, B_MN, AP, PROMOTE>;
+  auto* kernel = linear_tc_kernel<A_MN, B_MN, PLANES, PROMOTE>;
   cudaError_t rc = set_max_smem(reinterpret_cast<const void*>(kernel), T::kSmem);
   if (rc != cudaSuccess) return rc;
   rc = launch_after(kernel, dim3(2 * g.work.pairs), dim3(T::kThreads), T::kSmem, 2, st, tm_a, tm_b,
@@ -743,10 +756,10 @@ cudaError_t run(const LinearGemm& g, int* launches, cudaStream_t st) {
 
 template <bool A_MN, bool B_MN>
 cudaError_t promoted(const LinearGemm& g, int* launches, cudaStream_t st) {
-  if (g.steps.products > 1) return run<A_MN, B_MN, 2, true>(g, launches, st);
+  if (g.steps.products > 1) return run<A_MN, B_MN, true, true>(g, launches, st);
   // fp32 results; a bf16 result's own rounding hides the cuts.
-  return g.epi.y_f32 || (g.epi.pre && g.epi.pre_f32) ? run<A_MN, B_MN, 1, true>(g, launches, st)
-                                                     : run<A_MN, B_MN, 1, false>(g, launches, st);
+  return g.epi.y_f32 || (g.epi.pre && g.epi.pre_f32) ? run<A_MN, B_MN, false, true>(g, launches, st)
+                                                     : run<A_MN, B_MN, false, false>(g, launches, st);
 }
 
 }  // namespace
