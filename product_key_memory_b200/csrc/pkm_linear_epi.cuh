@@ -64,21 +64,22 @@ __device__ __forceinline__ float act_slope(float v, int act) {
   return 1.f;
 }
 
+__device__ __forceinline__ float load_as(const void* p, int64_t at, int f32) {
+  return f32 ? static_cast<const float*>(p)[at]
+             : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
+}
+__device__ __forceinline__ void store_as(void* p, int64_t at, int f32, float v) {
+  if (f32) static_cast<float*>(p)[at] = v;
+  else static_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(v);
+}
+
 __device__ __forceinline__ void linear_store1(const LinearEpilogue& e, int64_t at, int col,
                                               float v) {
   if (e.bias) v += __ldg(e.bias + col);
-  if (e.pre) {
-    if (e.pre_f32) static_cast<float*>(e.pre)[at] = v;
-    else static_cast<__nv_bfloat16*>(e.pre)[at] = __float2bfloat16_rn(v);
-  }
+  if (e.pre) store_as(e.pre, at, e.pre_f32, v);
   v = act_value(v, e.act);
-  if (e.y_f32) {
-    if (e.residual) v += static_cast<const float*>(e.residual)[at];
-    static_cast<float*>(e.y)[at] = v;
-  } else {
-    if (e.residual) v += __bfloat162float(static_cast<const __nv_bfloat16*>(e.residual)[at]);
-    static_cast<__nv_bfloat16*>(e.y)[at] = __float2bfloat16_rn(v);
-  }
+  if (e.residual) v += load_as(e.residual, at, e.y_f32);
+  store_as(e.y, at, e.y_f32, v);
 }
 
 // Eight consecutive columns of one row; `at` and `col` are multiples of 8.

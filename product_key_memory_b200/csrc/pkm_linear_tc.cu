@@ -241,16 +241,17 @@ __device__ __forceinline__ void add_bias32(const float* bias, int col, int N, fl
   }
 }
 
-__device__ __forceinline__ void activate32(int act, float* v) {
+template <int C>
+__device__ __forceinline__ void activate(int act, float* v) {
   if (act == PKM_ACT_RELU) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], PKM_ACT_RELU);
+    for (int i = 0; i < C; ++i) v[i] = act_value(v[i], PKM_ACT_RELU);
   } else if (act == PKM_ACT_GELU) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], PKM_ACT_GELU);
+    for (int i = 0; i < C; ++i) v[i] = act_value(v[i], PKM_ACT_GELU);
   } else if (act == PKM_ACT_SILU) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], PKM_ACT_SILU);
+    for (int i = 0; i < C; ++i) v[i] = act_value(v[i], PKM_ACT_SILU);
   }
 }
 
@@ -271,7 +272,7 @@ __device__ __forceinline__ void store_block(const CUtensorMap* tm_y, const CUten
     if (e.residual) stage_residual(y, e.residual, e.y_f32, row0, col, M, N, lane);
     if (e.bias) add_bias32(e.bias, col, N, v);
     if (e.pre) stage_row(p, lane, e.pre_f32, v);
-    activate32(e.act, v);
+    activate<32>(e.act, v);
     if (e.residual) {
       __syncwarp();   // the other lanes' chunks of this row
       add_residual(y, lane, e.y_f32, v);
@@ -296,11 +297,30 @@ __device__ __forceinline__ void store_block(const CUtensorMap* tm_y, const CUten
 #pragma unroll
   for (int i = 0; i < 32; ++i) sts_f32(base + (lane * 32 + (i ^ lane)) * 4, v[i]);
   __syncwarp();
-  if (col + lane < N) {
-    const int rows = min(32, M - row0);
-    for (int r = 0; r < rows; ++r)
-      linear_store1(e, static_cast<int64_t>(row0 + r) * N + col + lane, col + lane,
-                    lds_f32(base + (r * 32 + (lane ^ r)) * 4));
+  const bool mine = col + lane < N;
+  const float bias = e.bias && mine ? __ldg(e.bias + col + lane) : 0.f;
+  const int64_t at0 = static_cast<int64_t>(row0) * N + col + lane;
+  const int rows = mine ? min(32, M - row0) : 0;
+#pragma unroll 1
+  for (int r = 0; r < 32; r += 8) {
+    float u[8], res[8] = {};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = lds_f32(base + ((r + j) * 32 + (lane ^ (r + j))) * 4) + bias;
+    if (e.residual) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (r + j < rows) res[j] = load_as(e.residual, at0 + static_cast<int64_t>(r + j) * N, e.y_f32);
+    }
+    if (e.pre) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (r + j < rows) store_as(e.pre, at0 + static_cast<int64_t>(r + j) * N, e.pre_f32, u[j]);
+    }
+    activate<8>(e.act, u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (r + j < rows)
+        store_as(e.y, at0 + static_cast<int64_t>(r + j) * N, e.y_f32, u[j] + res[j]);
   }
 }
 
@@ -336,7 +356,7 @@ __device__ __forceinline__ void store_block64(uint32_t tmem, const CUtensorMap* 
       if (col + g * 32 >= N) continue;
       if (e.bias) add_bias32(e.bias, col + g * 32, N, v);
       if (pass) {
-        activate32(e.act, v);
+        activate<32>(e.act, v);
         if (e.residual) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
