@@ -170,7 +170,9 @@ cudaError_t pick_fwd(const FwdLaunch& l) {
   }
   if (d <= 32) return run_fwd<X, Y, 1, 4, 8>(l);
   if (d <= 128) return run_fwd<X, Y, 1, 4>(l);
-  if (d <= 16 * 32 * 8) return run_fwd<X, Y, 1, 8>(l);
+  if (d <= 256) return run_fwd<X, Y, 1, 8>(l);
+  // 512 columns a warp (65280 bf16 rows of 257: 45 us, with 256 columns 65; fp32 rows of 2001:
+  // 33 and 41).
   if (d <= 16 * 32 * 16) return run_fwd<X, Y, 1, 16>(l);
   return run_fwd<X, Y, 1, 32>(l);
 }
@@ -463,7 +465,9 @@ layernorm_backward_kernel(const void* gy, const void* x, const float* __restrict
   });
 }
 
-// Rows of any other length: one element at a time (a warp's accesses are contiguous).
+// Rows of other lengths up to 4096: one element at a time, straight into registers (a warp's
+// accesses are contiguous). 16760 bf16 rows of 1001: 52 us; by way of shared memory, as
+// below, 58.
 template <typename X, typename G, typename O, int C, bool WARPS>
 __global__ void __launch_bounds__(kMaxNormThreads)
 layernorm_backward_odd_kernel(const void* gy, const void* x, const float* __restrict__ mean,
@@ -540,6 +544,142 @@ layernorm_backward_odd_kernel(const void* gy, const void* x, const float* __rest
   });
 }
 
+// Rows of other lengths above 4096, a block each: it copies the 16-byte pieces that its next rows
+// touch into shared memory ahead of time, then works on single elements, contiguous over the
+// threads (3354 bf16 rows of 5001: 54 us; straight into registers, 16 at a time, 299). A row
+// begins anywhere in a piece.
+__host__ __device__ constexpr int row_window(int d, int size) {
+  return (d * size + 14) / 16 * 16 + 16;   // d * size bytes that start at most 15 into a block
+}
+// The blocks that hold `bytes` bytes from p, of an array that ends at `end`.
+__device__ __forceinline__ void copy_row(uint32_t dst, const char* p, int bytes, const char* end,
+                                         int t, int T) {
+  const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+  for (int i = t * 16; i < shift + bytes; i += T * 16) {
+    const char* q = p - shift + i;
+    const int64_t left = end - q;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i), "l"(q),
+                 "r"(left < 16 ? static_cast<int>(left) : 16)
+                 : "memory");
+  }
+}
+template <typename E> __device__ __forceinline__ float lds_elem(uint32_t at) {
+  if constexpr (kSize<E> == 4) {
+    float f;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(at) : "memory");
+    return f;
+  } else {
+    uint16_t h;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at) : "memory");
+    return __uint_as_float(static_cast<uint32_t>(h) << 16);
+  }
+}
+
+template <typename X, typename G, typename O, int C>
+__global__ void __launch_bounds__(kMaxNormThreads)
+layernorm_backward_wide_kernel(const void* gy, const void* x, const float* __restrict__ mean,
+                              const float* __restrict__ rstd, const float* __restrict__ gamma,
+                              const void* gsum, int gsum_f32, void* gx, float* part, int64_t rows,
+                              int d, int stages) {
+  extern __shared__ __align__(16) float sh[];   // the ring
+  __shared__ float4 red[2][kMaxNormThreads / 32];
+  constexpr int kX = kSize<X>, kG = kSize<G>;
+  constexpr bool kHold = C <= 16;   // xhat and t stay in registers; else they are made twice
+  constexpr int T = kMaxNormThreads;
+  const int t = threadIdx.x;
+  const float ninv_d = -1.f / static_cast<float>(d);
+  const int ks = gsum ? (gsum_f32 ? 4 : 2) : 0;
+  const int at_g = row_window(d, kX), at_s = at_g + row_window(d, kG);
+  const int stage = at_s + (ks ? row_window(d, ks) : 0);
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(sh));
+  float ag[C], ab[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) ag[c] = ab[c] = 0.f;
+  const int64_t stride = gridDim.x;
+  const char *cx = static_cast<const char*>(x), *cg = static_cast<const char*>(gy),
+             *cs = static_cast<const char*>(gsum);
+  int fill = 0;                                  // the slot that the next copy goes to
+  const auto prefetch = [&](int64_t row) {
+    if (row < rows) {
+      const uint32_t to = ring + fill * stage;
+      const int64_t at = row * d, n = rows * d;
+      copy_row(to, cx + at * kX, d * kX, cx + n * kX, t, T);
+      copy_row(to + at_g, cg + at * kG, d * kG, cg + n * kG, t, T);
+      if (ks) copy_row(to + at_s, cs + at * ks, d * ks, cs + n * ks, t, T);
+    }
+    copy_commit();                               // empty groups keep the count
+    if (++fill == stages) fill = 0;
+  };
+  int64_t row = blockIdx.x;
+  for (int k = 0; k < stages - 1; ++k) prefetch(row + k * stride);
+  float mu = __ldg(mean + row), rs = __ldg(rstd + row);   // no more blocks than rows
+  int slot = 0, flip = 0;
+  for (; row < rows; row += stride) {
+    if (stages == 1) {
+      __syncthreads();                                 // the row before has been read
+      prefetch(row);
+      copy_wait<0>();
+    } else if (stages == 2) {
+      copy_wait<0>();
+    } else {
+      copy_wait<1>();
+    }
+    __syncthreads();                                   // all threads' copies; the row before is free
+    if (stages > 1) prefetch(row + (stages - 1) * stride);
+    const bool more = row + stride < rows;
+    const float mu_next = more ? __ldg(mean + row + stride) : 0.f;
+    const float rs_next = more ? __ldg(rstd + row + stride) : 0.f;
+    const int64_t base = row * d;
+    // The element of column t.
+    const uint32_t in = ring + slot * stage;
+    const uint32_t sx = in + (static_cast<uint32_t>(base * kX) & 15) + t * kX;
+    const uint32_t sg = in + at_g + (static_cast<uint32_t>(base * kG) & 15) + t * kG;
+    const uint32_t ss = in + at_s + (static_cast<uint32_t>(base * ks) & 15) + t * ks;
+    float s1 = 0.f, s2 = 0.f;
+    float xh[kHold ? C : 1], tt[kHold ? C : 1];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int col = c * T + t;
+      if (col >= d) break;
+      const float q = (lds_elem<X>(sx + c * T * kX) - mu) * rs;
+      const float g = lds_elem<G>(sg + c * T * kG);
+      const float w = g * __ldg(gamma + col);
+      s1 += w;
+      s2 = fmaf(w, q, s2);
+      ag[c] = fmaf(g, q, ag[c]);
+      ab[c] += g;
+      if (kHold) xh[kHold ? c : 0] = q, tt[kHold ? c : 0] = w;
+    }
+    float a1[1] = {s1}, a2[1] = {s2};
+    row_sums<1, true>(a1, a2, T, 0, t >> 5, red[flip], ninv_d);
+    flip ^= 1;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int col = c * T + t;
+      if (col >= d) break;
+      const float q = kHold ? xh[kHold ? c : 0] : (lds_elem<X>(sx + c * T * kX) - mu) * rs;
+      const float w = kHold ? tt[kHold ? c : 0]
+                            : lds_elem<G>(sg + c * T * kG) * __ldg(gamma + col);
+      float o = rs * (w + a1[0] + q * a2[0]);
+      if (ks == 4) o += lds_elem<F32>(ss + c * T * 4);
+      else if (ks == 2) o += lds_elem<BF16>(ss + c * T * 2);
+      Out<O, 1>::store(gx, base + col, &o);
+    }
+    mu = mu_next, rs = rs_next;
+    if (++slot == stages) slot = 0;
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!part) return;
+  float* to = part + static_cast<int64_t>(blockIdx.x) * 2 * d;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int col = c * T + t;
+    if (col >= d) break;
+    to[col] = ag[c];
+    to[d + col] = ab[c];
+  }
+}
+
 // grad_gamma / grad_beta = column sums of the partial rows [blocks][2 d]: 32 columns a
 // block, 32 strands of rows per column, added in order.
 constexpr int kStrands = 32;
@@ -587,7 +727,7 @@ NormGroups norm_groups(int64_t rows, int d) {
     if (n.C == 1) n.R = 2;
   } else {
     n.C = d <= 64 ? 2 : (d <= 8 * kMaxNormThreads ? 8 : (d <= 16 * kMaxNormThreads ? 16 : 32));
-    n.T = round32((d + n.C - 1) / n.C);
+    n.T = n.C > 8 ? kMaxNormThreads : round32((d + n.C - 1) / n.C);
   }
   n.per = kMaxNormThreads / n.T;
   if (n.T > 32 && n.per > 8) n.per = 8;                  // barriers: one for each group
@@ -636,6 +776,21 @@ cudaError_t run_bwd_odd(const BwdLaunch& l, const NormGroups& n) {
   return cudaGetLastError();
 }
 
+template <typename X, typename G, typename O, int C>
+cudaError_t run_bwd_wide(const BwdLaunch& l, const NormGroups& n) {
+  const size_t row = row_window(l.d, kSize<X>) + row_window(l.d, kSize<G>) +
+                     (l.gsum ? row_window(l.d, l.gsum_f32 ? 4 : 2) : 0);
+  int stages = 1;                                        // 1: the widest rows, not ahead
+  while (stages < 3 && (stages + 1) * row <= kRingBytes) ++stages;
+  auto* kernel = layernorm_backward_wide_kernel<X, G, O, C>;
+  cudaError_t e = set_max_smem(reinterpret_cast<const void*>(kernel), stages * row);
+  if (e != cudaSuccess) return e;
+  kernel<<<n.blocks, kMaxNormThreads, stages * row, l.st>>>(l.gy, l.x, l.mean, l.rstd, l.gamma,
+                                                            l.gsum, l.gsum_f32, l.gx, l.part,
+                                                            l.rows, l.d, stages);
+  return cudaGetLastError();
+}
+
 template <typename X, typename G, typename O>
 cudaError_t pick_bwd(const BwdLaunch& l) {
   const NormGroups n = norm_groups(l.rows, l.d);
@@ -646,9 +801,10 @@ cudaError_t pick_bwd(const BwdLaunch& l) {
     return run_bwd<X, G, O, 4, true>(l, n);
   }
   if (n.C == 2) return run_bwd_odd<X, G, O, 2, false>(l, n);
+  if (n.C == 8 && n.T == 32) return run_bwd_odd<X, G, O, 8, false>(l, n);   // a warp: no barrier
   if (n.C == 8) return run_bwd_odd<X, G, O, 8, true>(l, n);
-  if (n.C == 16) return run_bwd_odd<X, G, O, 16, true>(l, n);
-  return run_bwd_odd<X, G, O, 32, true>(l, n);
+  if (n.C == 16) return run_bwd_wide<X, G, O, 16>(l, n);
+  return run_bwd_wide<X, G, O, 32>(l, n);
 }
 
 }  // namespace

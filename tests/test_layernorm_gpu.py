@@ -258,3 +258,22 @@ def test_another_stream_and_captured_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got + gotb, want + wantb))
+
+
+@pytest.mark.parametrize("rows,d", [(3000, 100), (5000, 255), (4000, 65), (6000, 33), (3000, 257),
+                                    (900, 1001), (700, 2001), (500, 5001), (300, 8191), (200, 16383)])
+@pytest.mark.parametrize("kinds", [(F32, F32, F32, F32), (BF16, BF16, None, BF16), (F32, BF16, BF16, F32)])
+def test_backward_many_rows_of_odd_widths(rows, d, kinds):
+    """Several rows a group and a block, all numbers of groups a block holds, and every place in a
+    16-byte block for a row to begin."""
+    import product_key_memory_b200 as P
+    xt, gt, st, ot = kinds
+    x, gsum, gamma, beta, rn = _data(rows, d, xt, st, seed=d + 2)
+    gy = rn(rows, d).to(gt)
+    _, _, mean, rstd = P.pkm_layernorm_forward(x, gamma, beta)
+    gx, check_x = guarded((rows, d), ot)
+    got = P.pkm_layernorm_backward(gy, x, mean, rstd, gamma, grad_sum=gsum, grad_x=gx)
+    _check_backward(gy, x, mean, rstd, gamma, gsum, got)
+    check_x()
+    a = P.pkm_layernorm_backward(gy, x, mean, rstd, gamma, grad_sum=gsum, grad_dtype=ot)
+    assert all(torch.equal(p, q) for p, q in zip(a, got))
