@@ -676,15 +676,19 @@ __global__ void __launch_bounds__(Tile<PLANES, PROMOTE>::kThreads, 1) linear_tc_
 }
 
 // Adds the parts of the cut tiles in order and applies the epilogue. Block: kJoinRows rows of
-// one tile, a thread for 8 columns.
+// one tile, a warp for a row: eight columns a lane side by side, or (rows of the output that
+// are no 16-byte multiples) 32 apart, so that every access is contiguous over the lanes.
 constexpr int kJoinRows = 4;
+template <bool APART>
 __global__ void __launch_bounds__(kJoinRows* BN / 8) linear_join_kernel(
     const float* part, const LinearWork plan, int mt, int nt, int M, int N,
     const LinearEpilogue epi) {
+  static_assert(BN == 256, "32 lanes of 8 columns");
   constexpr int kBlocks = 2 * kRows / kJoinRows;
   const int t = blockIdx.x / kBlocks;                    // of the cut tiles
-  const int row = (blockIdx.x % kBlocks) * kJoinRows + threadIdx.x / (BN / 8);
-  const int col = threadIdx.x % (BN / 8) * 8;
+  const int row = (blockIdx.x % kBlocks) * kJoinRows + threadIdx.x / 32;
+  const int lane = threadIdx.x & 31;
+  const int col = APART ? lane : lane * 8;
   const TileAt mn = tile_at(plan.whole + t, mt, nt);
   const int m = mn.m * (2 * kRows) + row, n = mn.n * BN + col;
   const int64_t p0 = static_cast<int64_t>(t) * plan.kblocks, p1 = p0 + plan.kblocks;
@@ -696,28 +700,46 @@ __global__ void __launch_bounds__(kJoinRows* BN / 8) linear_join_kernel(
   if (m >= M || n >= N || c0 == c1) return;              // c0 == c1: one pair had it all
   constexpr int64_t kPart = static_cast<int64_t>(2 * kRows) * BN;
   const float* q = part + static_cast<int64_t>(row) * BN + col;
+  const auto load = [](const float* p, float* v) {
+    if (APART) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = p[32 * i];
+    } else {
+      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+  };
   float v[8];
-  {
-    const float4* f = reinterpret_cast<const float4*>(q + first * kPart);
-    const float4 a = f[0], b = f[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  }
+  load(q + first * kPart, v);
 #pragma unroll 4
   for (int c = c0 + 1; c <= c1; ++c) {
-    const float4* f = reinterpret_cast<const float4*>(q + 2 * c * kPart);
-    const float4 a = f[0], b = f[1];
-    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    float u[8];
+    load(q + 2 * c * kPart, u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += u[i];
   }
   const int64_t at = static_cast<int64_t>(m) * N + n;
-  if ((N & 7) == 0) {
+  if (!APART) {
     linear_store8(epi, at, n, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (n + i < N) linear_store1(epi, at + i, n + i, v[i]);
+    return;
   }
+  float res[8] = {}, bias[8] = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (n + 32 * i >= N) break;
+    if (epi.residual) res[i] = load_as(epi.residual, at + 32 * i, epi.y_f32);
+    if (epi.bias) bias[i] = __ldg(epi.bias + n + 32 * i);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] += bias[i];
+    if (epi.pre && n + 32 * i < N) store_as(epi.pre, at + 32 * i, epi.pre_f32, v[i]);
+  }
+  activate<8>(epi.act, v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (n + 32 * i < N) store_as(epi.y, at + 32 * i, epi.y_f32, v[i] + res[i]);
 }
 
 // [planes][rows][cols] of an output or of the parts.
@@ -770,7 +792,8 @@ cudaError_t run(const LinearGemm& g, int* launches, cudaStream_t st) {
   const int mt = (g.M + 2 * kRows - 1) / (2 * kRows), nt = (g.N + BN - 1) / BN;
   const unsigned blocks = static_cast<unsigned>((mt * nt - g.work.whole) * (2 * kRows / kJoinRows));
   ++*launches;
-  return launch_after(linear_join_kernel, dim3(blocks), dim3(kJoinRows * BN / 8), 0, 1, st, g.part,
+  auto* join = g.N % 8 ? linear_join_kernel<true> : linear_join_kernel<false>;
+  return launch_after(join, dim3(blocks), dim3(kJoinRows * BN / 8), 0, 1, st, g.part,
                       g.work, mt, nt, g.M, g.N, g.epi);
 }
 
