@@ -297,7 +297,8 @@ int pkm_slot_usage(const pkm_shape* s, const int32_t* indices, unsigned long lon
 
 /* Layer norm sizes and types; every *_dtype is a pkm_dtype. */
 typedef struct {
-  int64_t rows;       /* rows (tokens); 0 is allowed, and then the per-row pointers may be NULL */
+  int64_t rows;       /* rows (tokens), < 2^31; 0 is allowed, and then the per-row pointers may be
+                         NULL */
   int32_t d;          /* row length, 1 <= d <= 16384 (PKM_ERR_UNSUPPORTED above) */
   int32_t x_dtype;    /* x and sum */
   int32_t add_dtype;  /* add; in the backward grad_sum */
@@ -355,8 +356,8 @@ enum { PKM_ACT_NONE = 0, PKM_ACT_RELU = 1, PKM_ACT_GELU = 2, PKM_ACT_SILU = 3 };
 
 /* Dense layer sizes and types. */
 typedef struct {
-  int64_t M;           /* rows (tokens), < 2^31; 0 is allowed, and then the per-row pointers may
-                          be NULL */
+  int64_t M;           /* rows (tokens), up to 2^31 - 257; 0 is allowed, and then the per-row
+                          pointers may be NULL */
   int32_t N;           /* output width, 1 <= N <= 2^20 */
   int32_t K;           /* input width, 1 <= K <= 2^20 */
   int32_t dtype;       /* pkm_dtype of x, W, pre and, in the backward, grad_y */
@@ -378,7 +379,7 @@ size_t pkm_linear_workspace_size(const pkm_linear_shape* s, int for_backward);
  * planes whose sum is the value to 2^-24, and the products above 2^-24 of the largest are
  * added; so an infinite operand makes its sums infinite or NaN. y is computed from pre
  * before pre is rounded. Up to 8 rows take a kernel that streams W once (in fp32
- * arithmetic). M < 2^31, and M, N and K with M N and M K below 2^38.
+ * arithmetic). M N and M K are below 2^38.
  * workspace: pkm_linear_workspace_size(s, 0) bytes, 256-byte aligned; its status word
  * (pkm_device_status) records a bounded wait that ran out.
  */
