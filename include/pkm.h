@@ -378,8 +378,8 @@ size_t pkm_linear_workspace_size(const pkm_linear_shape* s, int for_backward);
  * Products accumulate in fp32 on the tensor cores. fp32 operands are split into three bf16
  * planes whose sum is the value to 2^-24, and the products above 2^-24 of the largest are
  * added; so an infinite operand makes its sums infinite or NaN. y is computed from pre
- * before pre is rounded. Up to 8 rows take a kernel that streams W once (in fp32
- * arithmetic). M N and M K are below 2^38.
+ * before pre is rounded. Few rows (up to 8, in bf16 16 or 32) take kernels that stream W
+ * once. M N and M K are below 2^38.
  * workspace: pkm_linear_workspace_size(s, 0) bytes, 256-byte aligned; its status word
  * (pkm_device_status) records a bounded wait that ran out.
  */

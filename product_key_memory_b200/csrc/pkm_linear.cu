@@ -24,6 +24,15 @@ __device__ __forceinline__ void clear_status(int* status) {
   if (status && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = 0;
 }
 
+// v as bf16 planes hi, mid, lo (rounded to nearest, so the sum is v to 2^-24); a value
+// that hi cannot hold as finite leaves zeros below it.
+__device__ __forceinline__ void split(float v, float* p) {
+  p[0] = rounded<BF16>(v);
+  const bool fine = fabsf(p[0]) < __uint_as_float(0x7f800000u);
+  p[1] = fine ? rounded<BF16>(v - p[0]) : 0.f;
+  p[2] = fine ? rounded<BF16>(v - p[0] - p[1]) : 0.f;
+}
+
 // ---------------------------------------------------------------- small batches
 constexpr int kSmallCols = 4;
 
@@ -140,16 +149,150 @@ cudaError_t run_small(int M, const void* x, const void* W, int N, int K,
   }
 }
 
-// --------------------------------------------------------------- operand planes
-// v as bf16 planes hi, mid, lo (rounded to nearest, so the sum is v to 2^-24); a value
-// that hi cannot hold as finite leaves zeros below it.
-__device__ __forceinline__ void split(float v, float* p) {
-  p[0] = rounded<BF16>(v);
-  const bool fine = fabsf(p[0]) < __uint_as_float(0x7f800000u);
-  p[1] = fine ? rounded<BF16>(v - p[0]) : 0.f;
-  p[2] = fine ? rounded<BF16>(v - p[0] - p[1]) : 0.f;
+// --------------------------------------------------------------------- few rows
+// y^T = W x^T in bf16 on the warps' matrix instructions (m16n8k16): a warp has 16 rows of W, NT
+// tiles of 8 rows of x, and one of `slices` shares of K. Which k an instruction's
+// places stand for is free as long as W and x agree, so a lane's fragments are 16 bytes of a
+// row as they lie in memory: each lane copies its own into shared memory kStages pieces of 32
+// k ahead, with no barrier, which keeps enough of W in flight (two pieces ahead in registers
+// took twice as long). The accumulators are taken out every 4 pieces, as the tensor-core
+// kernel does; the slices' sums are added in order. Bound by W's bytes and, with
+// few of them, by latency: 16 rows, 1024 -> 4096: 4.7 us (256-row tiles 9.6), 4096 -> 4096 10 us,
+// 16384 -> 16384 106 us, 5.0 TB/s.
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+template <int NT> struct RowsTile {
+  static constexpr int kPieces = 2 + NT;                       // 512 bytes of a warp each
+  static constexpr int kStages = NT == 1 ? 8 : NT == 2 ? 6 : 4;
+  static constexpr int kValues = NT * 4;                       // sums of a lane
+  static constexpr size_t kSmem = kStages * kPieces * 512;     // of a warp
+  static_assert(kSmem >= kValues * 32 * sizeof(float), "the sums take the ring's place");
+};
+
+template <int NT>
+__global__ void __launch_bounds__(512) linear_rows_kernel(const uint16_t* x, const uint16_t* W,
+                                                          int M, int N, int K, int slices,
+                                                          const LinearEpilogue epi, int* status) {
+  using T = RowsTile<NT>;
+  extern __shared__ __align__(16) uint8_t ring_raw[];
+  let_next_in();
+  wait_for_previous();
+  clear_status(status);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, q = lane & 3;
+  const int groups = (blockDim.x >> 5) / slices, slice = warp % slices;
+  const int n0 = (blockIdx.x * groups + warp / slices) * 16;
+  const int share = (K + 32 * slices - 1) / (32 * slices) * 32;
+  const int begin = min(K, slice * share), end = min(K, begin + share);
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring_raw)) +
+                        warp * static_cast<uint32_t>(T::kSmem) + lane * 16;
+  // Rows past the end are the last one again; their sums are not stored.
+  const uint16_t *pw[2], *px[NT];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) pw[i] = W + static_cast<int64_t>(min(n0 + i * 8 + g, N - 1)) * K;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) px[j] = x + static_cast<int64_t>(min(j * 8 + g, M - 1)) * K;
+  int next = begin + q * 8;                            // this lane's next k to copy
+  uint32_t fill = 0;
+  const auto prefetch = [&] {
+    const int bytes = next < end ? 16 : 0;             // 0: zeros, nothing is read
+    const int at = next < end ? next : 0;
+    const uint32_t to = ring + fill * (T::kPieces * 512);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * 512),
+                   "l"(pw[i] + at), "r"(bytes)
+                   : "memory");
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(to + (2 + j) * 512),
+                   "l"(px[j] + at), "r"(bytes)
+                   : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    next += 32;
+    if (++fill == T::kStages) fill = 0;
+  };
+  const auto piece = [&](uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+  };
+#pragma unroll
+  for (int i = 0; i < T::kStages - 1; ++i) prefetch();
+  float sum[NT][4] = {}, c[NT][4] = {};
+  uint32_t slot = 0;
+  const int steps = (end - begin + 31) / 32;
+  for (int s = 0; s < steps; ++s) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(T::kStages - 2) : "memory");
+    const uint32_t at = ring + slot * (T::kPieces * 512);
+    const uint4 lo = piece(at), hi = piece(at + 512);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const uint4 b = piece(at + (2 + j) * 512);
+      mma16816(c[j], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+      mma16816(c[j], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+    }
+    prefetch();                                        // into the slot before this one
+    if (++slot == T::kStages) slot = 0;
+    if ((s & 3) == 3 || s + 1 == steps) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[j][i] += c[j][i], c[j][i] = 0.f;
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();                                     // the ring is free
+  float* sums = reinterpret_cast<float*>(ring_raw);    // [warp][value][lane]
+  float* mine = sums + warp * T::kValues * 32 + lane;
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mine[(j * 4 + i) * 32] = sum[j][i];
+  __syncthreads();
+  // The slices share the values of their group out.
+  const float* from = sums + (warp - slice) * T::kValues * 32 + lane;
+  for (int v = slice; v < T::kValues; v += slices) {
+    const int i = v & 3, j = v >> 2;
+    const int col = n0 + (i >> 1) * 8 + g, m = j * 8 + 2 * q + (i & 1);
+    if (col >= N || m >= M) continue;
+    float total = 0.f;
+    for (int w = 0; w < slices; ++w) total += from[(w * T::kValues + v) * 32];
+    linear_store1(epi, static_cast<int64_t>(m) * N + col, col, total);
+  }
+}
+
+template <int NT>
+cudaError_t run_rows(const void* x, const void* W, int M, int N, int K, const LinearEpilogue& epi,
+                     int* status, cudaStream_t st) {
+  // K is shared out until there are 8 warps an SM or a slice has less than 256 k; blocks of 16
+  // warps where all of them share a group's K (6400 -> 1600, 8 rows: 7.6 us, with 8 warps 9.5;
+  // 1600 -> 6400, which has 4 slices: 10.1 and 7.3).
+  const int64_t tiles = (N + 15) / 16;
+  int slices = 1;
+  while (slices < 16 && slices * 256 <= K && tiles * slices < 8 * sm_count()) slices *= 2;
+  const int warps = slices == 16 ? 16 : 8;
+  const int per = warps / slices * 16;
+  const size_t smem = warps * RowsTile<NT>::kSmem;
+  auto* kernel = linear_rows_kernel<NT>;
+  cudaError_t e = set_max_smem(reinterpret_cast<const void*>(kernel), 16 * RowsTile<NT>::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_after(kernel, dim3((N + per - 1) / per), dim3(32 * warps), smem, 1, st,
+                      static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(W), M, N, K,
+                      slices, epi, status);
+}
+
+// --------------------------------------------------------------- operand planes
 // Eight columns of a row from `col` (a multiple of 8) as loaded; columns from `cols` on are 0.
 // V = 8: the row is 16-byte aligned and the eight exist.
 template <typename E, int V> struct Chunk;
@@ -396,6 +539,15 @@ int slope_planes(const LinearArgs& a) {
   return a.N % 8 == 0 ? 0 : 1;
 }
 
+// The forward of few rows on the warps' matrix instructions: from 5 rows of bf16 on (4 rows, 4096
+// -> 1024: 5.4 us, the small-batch kernel 4.4), up to 16, or 32 where W is small enough that the
+// rereading of x (M / 16 times W's bytes) is hidden (32 rows, 4096 -> 4096: 15.3 us, the tensor-core
+// kernel 15.8; 4096 -> 8192: 24.6 and 21.5).
+bool linear_rows(const LinearArgs& a) {
+  return a.dtype == PKM_BF16 && a.K % 8 == 0 && a.M > 4 &&
+         (a.M <= 16 || (a.M <= 32 && static_cast<int64_t>(a.N) * a.K <= 1 << 24));
+}
+
 struct Layout {
   size_t x, W, d, part, bias, total;   // offsets; total = bytes
   LinearWork fwd, gx, gw;
@@ -435,7 +587,7 @@ Layout layout(const LinearArgs& a, bool backward) {
 
 }  // namespace
 
-bool linear_small(const LinearArgs& a) { return a.M <= kSmallM; }
+bool linear_small(const LinearArgs& a) { return a.M <= kSmallM || linear_rows(a); }
 
 size_t linear_workspace_bytes(const LinearArgs& a, bool backward) {
   if (a.M == 0 || (!backward && linear_small(a))) return kStatusBytes;
@@ -454,6 +606,11 @@ cudaError_t launch_linear_forward(const LinearArgs& a, const void* x, const void
     ++*launches;
     const int M = static_cast<int>(a.M);
     const bool vec = a.K % (a.dtype == PKM_F32 ? 4 : 8) == 0;   // rows of whole 16 bytes
+    if (linear_rows(a)) {
+      if (M <= 8) return run_rows<1>(x, W, M, a.N, a.K, epi, first, st);
+      if (M <= 16) return run_rows<2>(x, W, M, a.N, a.K, epi, first, st);
+      return run_rows<4>(x, W, M, a.N, a.K, epi, first, st);
+    }
     if (a.dtype == PKM_F32)
       return vec ? run_small<F32, 4>(M, x, W, a.N, a.K, epi, first, st)
                  : run_small<F32, 1>(M, x, W, a.N, a.K, epi, first, st);

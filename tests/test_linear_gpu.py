@@ -97,9 +97,39 @@ def test_forward_types_and_activations(kind, yt, name):
         _check_forward(x, W, None, None, name, y2, None)
 
 
+# Few rows: every number of row tiles and of shares of K, ragged in all three sizes, and the two
+# sides of each kernel's limits.
+FEW = [(5, 40, 8), (5, 1, 24), (6, 4096, 1024), (8, 16, 136), (9, 1600, 6400), (12, 33, 2056),
+       (13, 515, 264), (16, 100, 4096), (16, 2400, 520), (17, 100, 264), (24, 4100, 4104),
+       (31, 33, 40), (32, 515, 4096), (32, 4096, 1024), (33, 64, 512)]
+
+
+@pytest.mark.parametrize("M,N,K", FEW)
+@pytest.mark.parametrize("yt", [BF16, F32])
+def test_forward_few_rows(M, N, K, yt):
+    import product_key_memory_b200 as P
+    x, W, rn = _data(M, N, K, BF16, seed=4)
+    name = ACTS[(M + N) % 4]
+    bias = rn(N)
+    residual = rn(M, N).to(yt) if M % 2 else None
+    out, check_out = guarded((M, N), yt)
+    pre, check_pre = guarded((M, N), BF16)
+    shape = P.make_linear_shape(M, N, K, BF16, yt, name)
+    ws = P.alloc_linear_workspace(shape, False, "cuda").fill_(255)
+    P.pkm_linear_forward(x, W, bias, residual, name, out=out, pre=pre, workspace=ws)
+    assert P.pkm_device_status(ws) == 0
+    _check_forward(x, W, bias, residual, name, out, pre)
+    check_out()
+    check_pre()
+    x[M // 2] = float("inf")                       # the other rows stay as they are
+    again, _ = P.pkm_linear_forward(x, W, bias, residual, name, out_dtype=yt)
+    keep = torch.arange(M, device="cuda") != M // 2
+    assert torch.equal(again[keep], out[keep])
+
+
 def test_forward_residual_in_place_and_repeatable():
     import product_key_memory_b200 as P
-    for M in (6, 700):
+    for M in (6, 20, 700):
         x, W, rn = _data(M, 264, 512, BF16)
         residual = rn(M, 264).to(BF16)
         want, _ = P.pkm_linear_forward(x, W, None, residual, "gelu")
