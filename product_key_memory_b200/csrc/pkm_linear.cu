@@ -142,10 +142,16 @@ cudaError_t run_small(int M, const void* x, const void* W, int N, int K,
     case 2: return run(linear_small_kernel<E, V, 2>);
     case 3: return run(linear_small_kernel<E, V, 3>);
     case 4: return run(linear_small_kernel<E, V, 4>);
-    case 5: return run(linear_small_kernel<E, V, 5>);
-    case 6: return run(linear_small_kernel<E, V, 6>);
-    case 7: return run(linear_small_kernel<E, V, 7>);
-    default: return run(linear_small_kernel<E, V, 8>);
+  }
+  if constexpr (V == 8) {                    // bf16: linear_rows_kernel takes more
+    return cudaErrorInvalidValue;
+  } else {
+    switch (M) {
+      case 5: return run(linear_small_kernel<E, V, 5>);
+      case 6: return run(linear_small_kernel<E, V, 6>);
+      case 7: return run(linear_small_kernel<E, V, 7>);
+      default: return run(linear_small_kernel<E, V, 8>);
+    }
   }
 }
 
@@ -458,9 +464,9 @@ cudaError_t run_slope(int planes, const void* gy, const void* pre, int act, uint
   const dim3 grid(static_cast<unsigned>((rows + kPrepRows - 1) / kPrepRows),
                   static_cast<unsigned>((cols + 255) / 256));
   const int64_t ld = pad8(cols);
-  auto* kernel = planes == 0   ? linear_slope_kernel<E, V, 0>
-                 : planes == 1 ? linear_slope_kernel<E, V, 1>
-                               : linear_slope_kernel<E, V, 3>;
+  auto* kernel = planes == 0 ? linear_slope_kernel<E, V, 0> : linear_slope_kernel<E, V, 3>;
+  if constexpr (sizeof(typename E::T) == 2)   // fp32 layers use all planes
+    if (planes == 1) kernel = linear_slope_kernel<E, V, 1>;
   return launch_after(kernel, grid, 256, 0, 1, st, gy, pre, act, dst, part, rows, cols, ld, status);
 }
 
