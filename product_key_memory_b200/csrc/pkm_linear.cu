@@ -387,28 +387,39 @@ cudaError_t make_planes(const PlanesOf& a, const PlanesOf& b, int dtype, int col
 }
 
 // ------------------------------------------------------------ d = grad_y act'(pre)
-// Block: 256 columns (32 lanes of 8) x kPrepRows rows (8 warps, every eighth row each). d is
+// Block: 256 columns (32 lanes of 8) x `per` rows (8 warps, every eighth row each). d is
 // written as NP planes (NP = 0: not needed) and its column sums as one partial row per block
 // row (part NULL: not needed). Bound by HBM and the slope's arithmetic together: 4096 x 6400
 // bf16, gelu, three planes, 262 MB: 55 us with four blocks an SM, 60 with two of which each
 // thread has two rows in flight.
-constexpr int kPrepRows = 64;
+// Rows of a block: 64, or fewer (a warp then has fewer one after the other) until there are two
+// blocks for each of the 148 SMs (the whole backward of 560 x 120 -> 1240 fp32 silu: 36 us, with
+// 64 rows 50).
+int slope_rows(int64_t rows, int cols) {
+  int per = 64;
+  while (per > 8 && (rows + per - 1) / per * ((cols + 255) / 256) < 2 * 148) per /= 2;
+  return per;
+}
+int64_t slope_blocks(int64_t rows, int cols) {
+  const int per = slope_rows(rows, cols);
+  return (rows + per - 1) / per;
+}
 
 template <typename E, int V, int NP>
 __global__ void __launch_bounds__(256, 4) linear_slope_kernel(const void* gy, const void* pre,
                                                            int act, uint16_t* dst, float* part,
                                                            int64_t rows, int cols, int64_t ld,
-                                                           int* status) {
+                                                           int per, int* status) {
   __shared__ float sh[8][256];
   let_next_in();
   wait_for_previous();
   clear_status(status);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.y * 256 + lane * 8;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kPrepRows;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * per;
   float sum[8] = {};
   if (col < cols) {
-    const int64_t r1 = r0 + kPrepRows < rows ? r0 + kPrepRows : rows;
+    const int64_t r1 = r0 + per < rows ? r0 + per : rows;
     for (int64_t r = r0 + warp; r < r1; r += 8) {
       float g[8], t[8];
       Chunk<E, V> gc, tc;
@@ -461,13 +472,14 @@ __global__ void __launch_bounds__(256) linear_bias_kernel(const float* part, int
 template <typename E, int V>
 cudaError_t run_slope(int planes, const void* gy, const void* pre, int act, uint16_t* dst,
                       float* part, int64_t rows, int cols, int* status, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>((rows + kPrepRows - 1) / kPrepRows),
+  const dim3 grid(static_cast<unsigned>(slope_blocks(rows, cols)),
                   static_cast<unsigned>((cols + 255) / 256));
   const int64_t ld = pad8(cols);
   auto* kernel = planes == 0 ? linear_slope_kernel<E, V, 0> : linear_slope_kernel<E, V, 3>;
   if constexpr (sizeof(typename E::T) == 2)   // fp32 layers use all planes
     if (planes == 1) kernel = linear_slope_kernel<E, V, 1>;
-  return launch_after(kernel, grid, 256, 0, 1, st, gy, pre, act, dst, part, rows, cols, ld, status);
+  return launch_after(kernel, grid, 256, 0, 1, st, gy, pre, act, dst, part, rows, cols, ld,
+                      slope_rows(rows, cols), status);
 }
 
 // ------------------------------------------------------------------- host side
@@ -585,7 +597,7 @@ Layout layout(const LinearArgs& a, bool backward) {
     l.d = off;
     off += align256(static_cast<size_t>(a.M) * pad8(a.N) * 2 * d);
     l.bias = off;
-    off += align256(static_cast<size_t>((a.M + kPrepRows - 1) / kPrepRows) * a.N * 4);
+    off += align256(static_cast<size_t>(slope_blocks(a.M, a.N)) * a.N * 4);
   }
   l.total = off;
   return l;
@@ -671,7 +683,7 @@ cudaError_t launch_linear_backward(const LinearArgs& a, const void* x, const voi
     ++*launches;
     if (grad_bias) {
       e = launch_after(linear_bias_kernel, (a.N + 31) / 32, 256, 0, 1, st, part,
-                       (a.M + kPrepRows - 1) / kPrepRows, a.N, grad_bias);
+                       slope_blocks(a.M, a.N), a.N, grad_bias);
       if (e != cudaSuccess) return e;
       ++*launches;
     }

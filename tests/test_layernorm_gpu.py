@@ -277,3 +277,16 @@ def test_backward_many_rows_of_odd_widths(rows, d, kinds):
     check_x()
     a = P.pkm_layernorm_backward(gy, x, mean, rstd, gamma, grad_sum=gsum, grad_dtype=ot)
     assert all(torch.equal(p, q) for p, q in zip(a, got))
+
+
+@pytest.mark.parametrize("d", [129, 257, 301, 511, 513, 2001, 8191])
+@pytest.mark.parametrize("rows", [3, 900])
+def test_forward_odd_widths(rows, d):
+    import product_key_memory_b200 as P
+    types = [(F32, BF16, BF16), (BF16, F32, BF16), (BF16, None, F32), (F32, None, F32)]
+    xt, at, yt = types[(d // 2 + rows) % len(types)]
+    x, add, gamma, beta, _ = _data(rows, d, xt, at, seed=d + 3)
+    out, check = guarded((rows, d), yt)
+    got = P.pkm_layernorm_forward(x, gamma, beta, add=add, out=out)
+    _check_forward(x, add, gamma, beta, 1e-5, got)
+    check()
