@@ -366,7 +366,8 @@ typedef struct {
 } pkm_linear_shape;
 
 /* Bytes of workspace of pkm_linear_forward (for_backward = 0) or pkm_linear_backward (1);
- * 0 if the shape is invalid or not supported. */
+ * 0 if the shape is invalid or not supported. Fewer rows may need more (their products are
+ * cut into parts): a workspace for several M holds the largest of their sizes. */
 size_t pkm_linear_workspace_size(const pkm_linear_shape* s, int for_backward);
 
 /*
@@ -377,7 +378,8 @@ size_t pkm_linear_workspace_size(const pkm_linear_shape* s, int for_backward);
  * pkm_linear_backward takes.
  * Products accumulate in fp32 on the tensor cores. fp32 operands are split into three bf16
  * planes whose sum is the value to 2^-24, and the products above 2^-24 of the largest are
- * added; so an infinite operand makes its sums infinite or NaN. y is computed from pre
+ * added; so an infinite operand makes its sums infinite or NaN, and below 2^-100 an
+ * operand is its planes to 2^-134, not relatively. y is computed from pre
  * before pre is rounded. Few rows (up to 8, in bf16 16 or 32) take kernels that stream W
  * once. M N and M K are below 2^38.
  * workspace: pkm_linear_workspace_size(s, 0) bytes, 256-byte aligned; its status word
