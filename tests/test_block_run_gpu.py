@@ -6,15 +6,13 @@
 forward, backward from grad_y, and AdamW on every parameter; against 64-bit autograd with the
 memory's picks held fixed, and the step captured in a graph against the eager one.
 
-Tolerances (relative, 2-norm). fp32: a dense product of K terms is within
-2^-23 (6 K / 16 + 16) <= 2^-23 * 112 of sum |a b| (K <= 256); that sum is at most 8 times the
-result's size for sums of 256 terms of random sign (their ratio is near sqrt(2 K / pi) = 13 for
-worst rows, 0.8 sqrt(K) = 12.8 on average, and the error of rounded sums is random as well,
-below half its bound): 1e-4 a stage at most. Eight stages follow one another forward and
-backward (norm, memory, norm, dense, dense and back), norms and gelu pass relative errors on
-with a factor near 1: 1e-3. bf16: each of the eleven stored intermediates is off by at most 2^-9 of
-its own size (2^-10 on average), and the operands are the same as the oracle's: 11 * 2^-9 = 0.0215
-if all add up in one direction.
+Tolerances (relative, 2-norm). fp32: a product of K <= 256 terms is within 2^-23 (6 K / 16 + 16)
+<= 1.34e-5 of sum |a b|, which for terms of random sign is about 0.64 sqrt(K) <= 10.2 times the
+result: 1.4e-4 of it at most, were every step cut alike. Seven products lie on the longest way
+(q, W1, W2 forward; W2, W1, the memory's and q's backward); norms, softmax and gelu hand
+relative errors on with a factor near 1 and add a few 2^-24: 7 * 1.4e-4 = 1e-3.
+bf16: each of the eleven stored intermediates is off by at most 2^-9 of its own size, and the
+operands are the oracle's: 11 * 2^-9 = 0.0215 if all add up in one direction.
 """
 import pytest
 import torch
