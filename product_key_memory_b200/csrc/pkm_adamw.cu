@@ -18,7 +18,8 @@
 // fp32 states and masters (6.8 TB/s), 0.64 ms with 8-bit states (5.1 TB/s).
 //
 // With 8-bit states an element has 12 to 22 bytes and the arithmetic comes near the issue
-// rate (67 % of it, and 60 % of the DRAM's time), so it is kept short: a code's scale is folded into beta (powers of two: exact), an
+// rate (67 % of it, and 60 % of the DRAM's time), so it is kept short: a code's scale is
+// folded into beta (powers of two: exact, for the squares while they are normal numbers), an
 // element's root and quotient are the special function unit's (2^-23; only the block's
 // largest root, which decides the scale, is rounded exactly).
 #include <cuda_fp8.h>
@@ -235,6 +236,8 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
   constexpr bool gb = (KIND & kGradBf16) != 0, param_bf16 = (KIND & kParamBf16) != 0;
   constexpr bool pb = param_bf16 && !kWideMaster;   // type of what carries the parameter
   __shared__ float dynamic[2];   // 1 / (1 - b1^t), 1 / sqrt(1 - b2^t)
+  let_next_in();
+  wait_for_previous();
   float root = list.root, grad_scale = list.grad_scale, lr = 0.f, over = 1.f;
   uint32_t step32 = list.step32;
   if (list.dyn) {
@@ -443,7 +446,10 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
   }
 }
 
-constexpr int kSmallList = 16;     // 1.5 KB of parameters
+// Tensors of a launch, whose parameters (96 bytes a tensor) the host copies at each call: 48
+// vectors take 6.5 us of it with 64, 8.8 with 256.
+constexpr int kSmallList = 16;
+constexpr int kMediumList = 64;
 constexpr int kLargeList = 256;    // 25 KB (32,764 bytes is the limit)
 
 template <int CAP, int KIND>
@@ -452,8 +458,7 @@ cudaError_t launch_kind(const List<CAP>& list, cudaStream_t st) {
   // 32 blocks an SM going round, which spares most units the block's setup.
   const unsigned most = (KIND & kEight) ? static_cast<unsigned>(sm_count()) * 32 : 1u << 30;
   const unsigned grid = list.units < most ? list.units : most;
-  adamw_kernel<CAP, KIND><<<grid, kThreads, 0, st>>>(list);
-  return cudaGetLastError();
+  return launch_after(adamw_kernel<CAP, KIND>, dim3(grid), dim3(kThreads), 0, 1, st, list);
 }
 
 constexpr int kKinds = 16;
@@ -545,8 +550,9 @@ cudaError_t run_lists(const AdamWTensor* t, int64_t count, const AdamWHyper& h, 
 
 cudaError_t launch_adamw(const AdamWTensor* t, int64_t count, const AdamWHyper& h,
                          const float* dyn, int* launches, cudaStream_t st) {
-  return count <= kSmallList ? run_lists<kSmallList>(t, count, h, dyn, launches, st)
-                             : run_lists<kLargeList>(t, count, h, dyn, launches, st);
+  if (count <= kSmallList) return run_lists<kSmallList>(t, count, h, dyn, launches, st);
+  if (count <= kMediumList) return run_lists<kMediumList>(t, count, h, dyn, launches, st);
+  return run_lists<kLargeList>(t, count, h, dyn, launches, st);
 }
 
 }  // namespace pkm

@@ -52,6 +52,8 @@ layernorm_forward_kernel(const void* x, const void* add, int add_f32,
                          void* sum, float* mean_out, float* rstd_out, int64_t rows, int d, int wide,
                          float eps) {
   __shared__ float red[2][kMaxNormThreads / 32];
+  let_next_in();
+  wait_for_previous();
   const int lane = threadIdx.x & (LANES - 1), part = threadIdx.x / LANES;
   const int group = part / wide, w = part - group * wide;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / (LANES * wide)) + group;
@@ -151,10 +153,9 @@ cudaError_t run_fwd(const FwdLaunch& l) {
   const int per = LANES * wide >= 256 ? 1 : 256 / (LANES * wide);
   const int threads = round32(LANES * wide * per);
   const int64_t blocks = (l.rows + per - 1) / per;
-  layernorm_forward_kernel<X, Y, V, H, LANES>
-      <<<static_cast<unsigned>(blocks), threads, 0, l.st>>>(
-      l.x, l.add, l.add_f32, l.gamma, l.beta, l.y, l.sum, l.mean, l.rstd, l.rows, l.d, wide, l.eps);
-  return cudaGetLastError();
+  return launch_after(layernorm_forward_kernel<X, Y, V, H, LANES>, dim3(static_cast<unsigned>(blocks)),
+                      dim3(threads), 0, 1, l.st, l.x, l.add, l.add_f32, l.gamma, l.beta, l.y, l.sum,
+                      l.mean, l.rstd, l.rows, l.d, wide, l.eps);
 }
 
 template <typename X, typename Y>
@@ -297,6 +298,7 @@ layernorm_backward_kernel(const void* gy, const void* x, const float* __restrict
                           int d, int T, int per, int stages) {
   extern __shared__ __align__(16) float sh[];   // the ring; at the end the groups' column sums
   __shared__ float4 red[2][kMaxNormThreads / 32];
+  wait_for_previous();
   constexpr int R = C == 1 ? 2 : 1;
   constexpr int kX = kSize<X>, kG = kSize<G>, kO = kSize<O>;
   const int group = threadIdx.x / T;
@@ -450,7 +452,7 @@ layernorm_backward_kernel(const void* gy, const void* x, const float* __restrict
     slot += R * C * span;
     if (slot == ring_end) slot = ring;
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_in();
   if (!part) return;
   copy_wait<0>();
   __syncthreads();                                     // the ring is free
@@ -478,6 +480,7 @@ layernorm_backward_odd_kernel(const void* gy, const void* x, const float* __rest
                               int d, int T, int per) {
   extern __shared__ float sh[];   // the groups' column sums
   __shared__ float4 red[2][kMaxNormThreads / 32];
+  wait_for_previous();
   const int group = threadIdx.x / T;
   const int t = threadIdx.x - group * T;
   const float inv_d = 1.f / static_cast<float>(d);
@@ -533,7 +536,7 @@ layernorm_backward_odd_kernel(const void* gy, const void* x, const float* __rest
       Out<O, 1>::store(gx, base + col, &o);
     }
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_in();
   if (!part) return;
   store_part(part, sh, d, group, per, [&](float* to) {
 #pragma unroll
@@ -585,6 +588,7 @@ layernorm_backward_wide_kernel(const void* gy, const void* x, const float* __res
                               int d, int stages) {
   extern __shared__ __align__(16) float sh[];   // the ring
   __shared__ float4 red[2][kMaxNormThreads / 32];
+  wait_for_previous();
   constexpr int kX = kSize<X>, kG = kSize<G>;
   constexpr bool kHold = C <= 16;   // xhat and t stay in registers; else they are made twice
   constexpr int T = kMaxNormThreads;
@@ -670,7 +674,7 @@ layernorm_backward_wide_kernel(const void* gy, const void* x, const float* __res
     mu = mu_next, rs = rs_next;
     if (++slot == stages) slot = 0;
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_in();
   if (!part) return;
   float* to = part + static_cast<int64_t>(blockIdx.x) * 2 * d;
 #pragma unroll
@@ -688,7 +692,7 @@ constexpr int kStrands = 32;
 __global__ void __launch_bounds__(32 * kStrands) layernorm_columns_kernel(const float* part,
                                                                          int blocks, int d,
                                                                          float* gg, float* gb) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_previous();
   __shared__ float sh[kStrands][33];
   const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + c;
@@ -764,18 +768,16 @@ cudaError_t run_bwd(const BwdLaunch& l, const NormGroups& n) {
   auto* kernel = layernorm_backward_kernel<X, G, O, C, WARPS>;
   cudaError_t e = set_max_smem(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
-  kernel<<<n.blocks, threads, smem, l.st>>>(l.gy, l.x, l.mean, l.rstd, l.gamma, l.gsum, l.gsum_f32,
-                                            l.gx, l.part, l.rows, l.d, n.T, n.per, stages);
-  return cudaGetLastError();
+  return launch_after(kernel, dim3(n.blocks), dim3(threads), smem, 1, l.st, l.gy, l.x, l.mean, l.rstd,
+                      l.gamma, l.gsum, l.gsum_f32, l.gx, l.part, l.rows, l.d, n.T, n.per, stages);
 }
 
 template <typename X, typename G, typename O, int C, bool WARPS>
 cudaError_t run_bwd_odd(const BwdLaunch& l, const NormGroups& n) {
   const size_t smem = n.per > 1 ? static_cast<size_t>(n.per) * 2 * l.d * sizeof(float) : 0;
-  layernorm_backward_odd_kernel<X, G, O, C, WARPS><<<n.blocks, n.T * n.per, smem, l.st>>>(
-      l.gy, l.x, l.mean, l.rstd, l.gamma, l.gsum, l.gsum_f32, l.gx, l.part, l.rows, l.d, n.T,
-      n.per);
-  return cudaGetLastError();
+  return launch_after(layernorm_backward_odd_kernel<X, G, O, C, WARPS>, dim3(n.blocks),
+                      dim3(n.T * n.per), smem, 1, l.st, l.gy, l.x, l.mean, l.rstd, l.gamma, l.gsum,
+                      l.gsum_f32, l.gx, l.part, l.rows, l.d, n.T, n.per);
 }
 
 template <typename X, typename G, typename O, int C>
@@ -787,10 +789,8 @@ cudaError_t run_bwd_wide(const BwdLaunch& l, const NormGroups& n) {
   auto* kernel = layernorm_backward_wide_kernel<X, G, O, C>;
   cudaError_t e = set_max_smem(reinterpret_cast<const void*>(kernel), stages * row);
   if (e != cudaSuccess) return e;
-  kernel<<<n.blocks, kMaxNormThreads, stages * row, l.st>>>(l.gy, l.x, l.mean, l.rstd, l.gamma,
-                                                            l.gsum, l.gsum_f32, l.gx, l.part,
-                                                            l.rows, l.d, stages);
-  return cudaGetLastError();
+  return launch_after(kernel, dim3(n.blocks), dim3(kMaxNormThreads), stages * row, 1, l.st, l.gy, l.x,
+                      l.mean, l.rstd, l.gamma, l.gsum, l.gsum_f32, l.gx, l.part, l.rows, l.d, stages);
 }
 
 template <typename X, typename G, typename O>
@@ -840,17 +840,8 @@ cudaError_t launch_layernorm_backward(const NormArgs& a, const void* grad_y, con
   }
   if (e != cudaSuccess || !sums) return e;
   // Scheduled while the last rows are written; waits on the device for their end.
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((2 * a.d + 31) / 32);
-  cfg.blockDim = dim3(32 * kStrands);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, layernorm_columns_kernel, static_cast<const float*>(part),
-                            l.blocks, a.d, grad_gamma, grad_beta);
+  return launch_after(layernorm_columns_kernel, dim3((2 * a.d + 31) / 32), dim3(32 * kStrands), 0, 1,
+                      st, static_cast<const float*>(part), l.blocks, a.d, grad_gamma, grad_beta);
 }
 
 }  // namespace pkm
