@@ -3,14 +3,14 @@
 // Forward, per row:  h = x + add, mean = sum h / d, rstd = 1/sqrt(sum (h - mean)^2 / d + eps),
 // y = (h - mean) rstd gamma + beta. The row is read once and stays in registers for the
 // three uses; a row belongs to T threads (a part of a warp, a warp, or several warps). Bound
-// by HBM: 16384 rows of 1024, fp32 x, add and h, bf16 y: 41 us, 5.7 TB/s.
+// by HBM: 16384 rows of 1024, fp32 x, add and h, bf16 y: 40 us, 5.9 TB/s.
 //
 // Backward, per row, with xhat = (x - mean) rstd and t = grad_y gamma:
 //   grad_x = rstd (t - sum t / d - xhat sum (t xhat) / d) + grad_sum
 // and over the rows grad_gamma = sum grad_y xhat, grad_beta = sum grad_y. A group of T
 // threads keeps the same columns for all of its rows, so the column sums stay in its
 // registers; each block writes one partial row, and a second kernel adds the partial
-// rows in a fixed order. 16384 rows of 1600, fp32 grad_y, the others bf16: 60 us, 4.4 TB/s;
+// rows in a fixed order. 16384 rows of 1600, fp32 grad_y, the others bf16: 58 us, 4.5 TB/s;
 // the row's reduction, between its reads and its writes, keeps it from the copy's rate.
 #include "pkm_block.h"
 #include "pkm_elem.cuh"
