@@ -235,6 +235,27 @@ def test_backward_types_and_subsets(kind, xt, name):
             assert torch.equal(some[k], full[k]), k
 
 
+@pytest.mark.parametrize("name", ["relu", "gelu", "silu"])
+@pytest.mark.parametrize("M,N,K", [(2, 1101, 72), (33, 360, 464), (130, 513, 200), (700, 1304, 520)])
+def test_bf16_grad_x_is_its_own_rounding(name, M, N, K):
+    """d enters a bf16 grad_x as two planes, d to 2^-16 (each plane leaves at most half a step of
+    bf16, 2^-8, of what it stands for), so a result is the 64-bit one to its own half step and
+    _check_backward's other terms; d as one plane would be another 2^-8 of each product."""
+    import product_key_memory_b200 as P
+    x, W, rn = _data(M, N, K, BF16, seed=6)
+    pre, gy = rn(M, N).to(BF16), rn(M, N).to(BF16)
+    d = gy.double() * act_slope(pre.double(), name)
+    dd = gy.double().abs() * 10 * U * 1.13 if name != "relu" else U * d.abs()
+    b = _product_bound(d.abs() @ W.double().abs(), N, 2, 2.0 ** -16) + dd @ W.double().abs()
+    r = d @ W.double()
+    both = dict(x=torch.empty_like(x), W=torch.empty(N, K, device="cuda"))
+    alone = dict(x=torch.empty_like(x))
+    for grads in (both, alone):
+        P.pkm_linear_backward(x, W, gy, grads, pre=pre, activation=name)
+        assert_within("grad_x", grads["x"], r, b + half_step(BF16) * (r.abs() + b))
+    assert torch.equal(both["x"], alone["x"])
+
+
 def test_backward_against_differences():
     """Central differences of sum(y gy) in 64 bits against the kernel's gradients along random
     directions, gelu."""
