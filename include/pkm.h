@@ -439,8 +439,8 @@ typedef struct {
  * One AdamW step (Loshchilov and Hutter, decoupled weight decay) over a list of tensors:
  *   g = grad grad_scale,  m <- beta1 m + (1 - beta1) g,  v <- beta2 v + (1 - beta2) g^2
  *   p <- p (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
- * in fp32, with lr = hyper.lr lr_scale (square roots and quotients to 2^-22; second
- * moments of 8-bit states that are below 2^-110 to fewer bits). The moments that move p are
+ * in fp32, with lr = hyper.lr lr_scale (quotients, and square roots of fp32 states, to 2^-22;
+ * second moments of 8-bit states that are below 2^-110 to fewer bits). The moments that move p are
  * the new ones before they are rounded to 8 bits.
  * 8-bit states (after the block-wise states of Dettmers et al., "8-bit Optimizers via
  * Block-wise Quantization"): m and r = sqrt(v) as fp8 e4m3 codes, each block of 256

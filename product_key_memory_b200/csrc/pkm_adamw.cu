@@ -10,18 +10,20 @@
 // block takes units b, b + grid, ... and finds a unit's tensor by its first unit. A
 // warp owns 256 consecutive elements, 8 per lane, which is also the block that shares
 // a scale of 8-bit states: its largest magnitude is one warp reduction of the fp32 bits
-// (ordered like the magnitudes, NaN above all). m, v, the codes of m and the scales are
-// computed in single operations rounded to nearest (no fused multiply-add), so they are
-// the same bits as the formula evaluated step by step in fp32.
+// (ordered like the magnitudes, NaN above all). m, v, the codes and the scales are
+// computed in single operations rounded to nearest (no fused multiply-add, but for the dither's
+// sum, whose product is exact), so they are the same bits as the formula evaluated step by
+// step in fp32.
 //
 // Measured on the tensors of a 512^2 layer with their vectors, 271 M elements: 1.35 ms with
-// fp32 states and masters (6.8 TB/s), 0.64 ms with 8-bit states (5.1 TB/s).
+// fp32 states and masters (6.8 TB/s), 0.66 ms with 8-bit states (5.0 TB/s).
 //
 // With 8-bit states an element has 12 to 22 bytes and the arithmetic comes near the issue
-// rate (67 % of it, and 60 % of the DRAM's time), so it is kept short: a code's scale is
-// folded into beta (powers of two: exact, for the squares while they are normal numbers), an
-// element's root and quotient are the special function unit's (2^-23; only the block's
-// largest root, which decides the scale, is rounded exactly).
+// rate (66 % of it, and 53 % of the DRAM's time), so it is kept short: a code's scale is
+// folded into beta (powers of two: exact, for the squares while they are normal numbers) and an
+// element's quotient is the special function unit's (2^-23). Its root decides a code and is
+// rounded to nearest: with the special function unit's, 5 % faster, 4 codes in a million fell
+// the other way. With fp32 states, whose root only moves p, that one is used.
 #include <cuda_fp8.h>
 
 #include <math.h>
@@ -104,11 +106,6 @@ __device__ __forceinline__ void widen8(uint2 codes, float* f) {
 __device__ __forceinline__ float sqrt_fast(float x) {
   float y;
   asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float sqrt_normal(float x) {   // x not subnormal: a third of the code
-  float y;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float rcp_fast(float x) {
@@ -360,14 +357,14 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
           const Pair q = Pair(v[j], v[j + 1]) * o;
-          r[j] = sqrt_normal(q.lo());
-          r[j + 1] = sqrt_normal(q.hi());
+          r[j] = __fsqrt_rn(q.lo());
+          r[j + 1] = __fsqrt_rn(q.hi());
         }
       }
     }
     if (!fast) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) r[j] = sqrt_fast(v[j]);
+      for (int j = 0; j < 8; ++j) r[j] = eight ? __fsqrt_rn(v[j]) : sqrt_fast(v[j]);
     }
     const Pair roots(root * scale_r), eps(list.eps), keeps(keep), steps(-step);
 #pragma unroll

@@ -105,6 +105,19 @@ def test_first_steps_from_zero_states():
             _check(t, before[i], hyper, i)
 
 
+def test_every_code_of_a_long_tensor():
+    """Roots are rounded to nearest before their dither, so every code of the second moment is the
+    plain form's, however near to the middle of two codes its value lies."""
+    import product_key_memory_b200 as P
+    ts = [_tensor(P, n, F32, F32, 8, seed=n)[0] for n in (8 << 20, (4 << 20) + 77)]
+    before = [_copy(t) for t in ts]
+    P.pkm_adamw_step(P.make_adamw_tensors(ts), **HYPER)
+    for i, t in enumerate(ts):
+        want = adamw(before[i], HYPER, i)
+        for k in ("m", "v", "m_scale", "v_scale"):
+            assert _equal(t[k], want[k]), k
+
+
 def test_mixed_long_list():
     """More tensors than one launch takes, of every kind, empty ones among them."""
     import product_key_memory_b200 as P
