@@ -290,3 +290,23 @@ def test_forward_odd_widths(rows, d):
     got = P.pkm_layernorm_forward(x, gamma, beta, add=add, out=out)
     _check_forward(x, add, gamma, beta, 1e-5, got)
     check()
+
+
+@pytest.mark.parametrize("d", [64, 65, 520, 777, 1024, 1600, 4104, 5001, 8200, 16384])
+@pytest.mark.parametrize("rows", [5, 400])
+@pytest.mark.parametrize("xt,offset", [(F32, 1000.0), (F32, -30.0), (BF16, 30.0)])
+def test_backward_rows_far_from_zero(d, rows, xt, offset):
+    """Rows whose mean is many deviations: xhat is the difference x - mean, rounded relative to
+    itself, times rstd, so the column sums' terms are good relative to |grad_y xhat|, whatever
+    the mean."""
+    import product_key_memory_b200 as P
+    x, _, gamma, beta, rn = _data(rows, d, F32, None, seed=d + 4, scale=1.0)
+    x = (x + offset).to(xt)
+    gy = rn(rows, d)
+    _, _, mean, rstd = P.pkm_layernorm_forward(x, gamma, beta)
+    got = P.pkm_layernorm_backward(gy, x, mean, rstd, gamma)
+    _check_backward(gy, x, mean, rstd, gamma, None, got)
+    _, rg, _ = layernorm_backward(gy, x, mean, rstd, gamma, None)
+    xhat = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    # A term has two roundings of xhat and one of its product (or none, fused), the sum `rows` at most.
+    assert_within("grad_gamma", got[1], rg, (rows + 3) * U * (gy.double() * xhat).abs().sum(0))
