@@ -414,7 +414,8 @@ def pkm_trace_read(pass_: int = 0, max_stages: int = 4):
 # ---------------------------------------------------------------------------------------
 # The transformer block around the layer. These calls check the tensors they are given
 # (device, type, shape, contiguity: ValueError) and run on the device of their first
-# tensor, whichever device is current.
+# tensor, whichever device is current. With a `stream` other than the current one the inputs have
+# to be ready there and to live until it has read them, and results are ready on it.
 # ---------------------------------------------------------------------------------------
 _DTYPES = {torch.float32: PKM_F32, torch.bfloat16: PKM_BF16}
 
@@ -453,42 +454,45 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 
 
 class _Call:
-    """The device and stream of one call: makes `device` current while it lasts, and keeps
-    what the call allocates from being reused before `stream` is done with it."""
-    __slots__ = ("device", "given", "handle", "guard")
+    """The device and stream of one call: makes `device` current while it lasts, and a `stream`
+    that is not the current one too: what the call allocates then comes from that stream's
+    memory, which no work queued elsewhere still uses."""
+    __slots__ = ("device", "given", "handle", "guard", "caller")
 
     def __init__(self, device: torch.device, stream):
         if stream is not None and stream.device != device:
             raise ValueError("stream is on %s, not on %s" % (stream.device, device))
-        self.device, self.given, self.guard = device, stream, None
+        self.device, self.given, self.guard, self.caller = device, stream, None, None
 
     def __enter__(self):
         index = self.device.index
-        if _current_device() != index:
+        self.handle = _raw_stream(index)
+        if self.given is not None and self.given.cuda_stream != self.handle:
+            self.handle = self.given.cuda_stream
+            self.caller = torch.cuda.current_stream(index)
+            self.guard = torch.cuda.stream(self.given)
+            self.guard.__enter__()
+        elif _current_device() != index:
             self.guard = torch.cuda.device(index)
             self.guard.__enter__()
-        self.handle = _raw_stream(index)
-        if self.given is not None:
-            if self.given.cuda_stream == self.handle:
-                self.given = None
-            else:
-                self.handle = self.given.cuda_stream
         return self
 
     def __exit__(self, *exc):
         if self.guard is not None:
             self.guard.__exit__(*exc)
 
-    def empty(self, like: torch.Tensor, shape, dtype) -> torch.Tensor:
-        """An uninitialised tensor beside `like` (the forms that cost the host least)."""
+    def empty(self, like: torch.Tensor, shape, dtype, result: bool = True) -> torch.Tensor:
+        """An uninitialised tensor beside `like` (the forms that cost the host least). A result is
+        the caller's from then on: its memory waits for the work of the caller's stream when it
+        is dropped."""
         if dtype is not like.dtype:
             t = like.new_empty(shape, dtype=dtype)
         elif shape == like.shape:
             t = torch.empty_like(like)
         else:
             t = like.new_empty(shape)
-        if self.given is not None:
-            t.record_stream(self.given)
+        if result and self.caller is not None:
+            t.record_stream(self.caller)
         return t
 
 
@@ -607,7 +611,7 @@ def pkm_layernorm_backward(grad_y: torch.Tensor, x: torch.Tensor, mean: torch.Te
         if grad_beta is None:
             grad_beta = c.empty(gamma, (d,), torch.float32)
         if workspace is None:
-            workspace = c.empty(x, (max(need, 1),), torch.uint8)
+            workspace = c.empty(x, (max(need, 1),), torch.uint8, result=False)
         ws, nbytes = _given_workspace(c, workspace)
         rc = lib().pkm_layernorm_backward(ref, _addr(grad_y), _addr(x),
                                           _addr(mean), _addr(rstd), _addr(gamma), _addr(grad_sum),
@@ -758,7 +762,7 @@ def _linear_ref(for_backward, *fields):
 def _linear_workspace(c: _Call, x, workspace, need: int):
     """(workspace, bytes): the caller's, or one for this call."""
     if workspace is None:
-        return c.empty(x, (max(need, 1),), torch.uint8), need
+        return c.empty(x, (max(need, 1),), torch.uint8, result=False), need
     return _given_workspace(c, workspace)
 
 
