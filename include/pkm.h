@@ -351,7 +351,9 @@ int pkm_layernorm_backward(const pkm_norm_shape* s, const void* grad_y, const vo
                            void* stream);
 
 /* Activations of the dense layer: relu; gelu(v) = v Phi(v) with the normal distribution
- * Phi (not its tanh approximation); silu(v) = v / (1 + exp(-v)). */
+ * Phi (not its tanh approximation); silu(v) = v / (1 + exp(-v)). fp32 results of gelu and silu,
+ * and each term of their slopes, are within 2^-19 of themselves while Phi or exp(v) is above
+ * 2^-126 (0 below); bf16 results within 2^-15 before they are rounded. */
 enum { PKM_ACT_NONE = 0, PKM_ACT_RELU = 1, PKM_ACT_GELU = 2, PKM_ACT_SILU = 3 };
 
 /* Dense layer sizes and types. */

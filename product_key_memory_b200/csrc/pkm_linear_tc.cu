@@ -241,22 +241,23 @@ __device__ __forceinline__ void add_bias32(const float* bias, int col, int N, fl
   }
 }
 
-template <int C>
+template <bool FINE, int C>
 __device__ __forceinline__ void activate(int act, float* v) {
   if (act == PKM_ACT_RELU) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) v[i] = act_value(v[i], PKM_ACT_RELU);
+    for (int i = 0; i < C; ++i) v[i] = act_value<FINE>(v[i], PKM_ACT_RELU);
   } else if (act == PKM_ACT_GELU) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) v[i] = act_value(v[i], PKM_ACT_GELU);
+    for (int i = 0; i < C; ++i) v[i] = act_value<FINE>(v[i], PKM_ACT_GELU);
   } else if (act == PKM_ACT_SILU) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) v[i] = act_value(v[i], PKM_ACT_SILU);
+    for (int i = 0; i < C; ++i) v[i] = act_value<FINE>(v[i], PKM_ACT_SILU);
   }
 }
 
 // 32 rows x 32 columns of the result: this thread's row `row0 + lane` in v, columns from
-// `col`. Warp-uniform arguments but v.
+// `col`. Warp-uniform arguments but v. FINE: activations for fp32 outputs.
+template <bool FINE>
 __device__ __forceinline__ void store_block(const CUtensorMap* tm_y, const CUtensorMap* tm_pre,
                                             const LinearEpilogue& e, Outputs& o, int row0, int col,
                                             int M, int N, int lane, float* v) {
@@ -272,7 +273,7 @@ __device__ __forceinline__ void store_block(const CUtensorMap* tm_y, const CUten
     if (e.residual) stage_residual(y, e.residual, e.y_f32, row0, col, M, N, lane);
     if (e.bias) add_bias32(e.bias, col, N, v);
     if (e.pre) stage_row(p, lane, e.pre_f32, v);
-    activate<32>(e.act, v);
+    activate<FINE, 32>(e.act, v);
     if (e.residual) {
       __syncwarp();   // the other lanes' chunks of this row
       add_residual(y, lane, e.y_f32, v);
@@ -316,7 +317,7 @@ __device__ __forceinline__ void store_block(const CUtensorMap* tm_y, const CUten
       for (int j = 0; j < 8; ++j)
         if (r + j < rows) store_as(e.pre, at0 + static_cast<int64_t>(r + j) * N, e.pre_f32, u[j]);
     }
-    activate<8>(e.act, u);
+    activate<FINE, 8>(e.act, u);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (r + j < rows)
@@ -356,7 +357,7 @@ __device__ __forceinline__ void store_block64(uint32_t tmem, const CUtensorMap* 
       if (col + g * 32 >= N) continue;
       if (e.bias) add_bias32(e.bias, col + g * 32, N, v);
       if (pass) {
-        activate<32>(e.act, v);
+        activate<false, 32>(e.act, v);
         if (e.residual) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -649,8 +650,10 @@ __global__ void __launch_bounds__(Tile<PLANES, PROMOTE>::kThreads, 1) linear_tc_
               if (lane == 0) mbar_arrive_cluster(leader_addr(&tempty[buf]));
             }
             if (row0 >= M || n0 + g * 32 >= N) continue;
-            if (pc.slot < 0) store_block(&tm_y, &tm_pre, epi, o, row0, n0 + g * 32, M, N, lane, v);
-            else store_part(&tm_part, o, pc.slot, prow, pcol + g * 32, lane, v);
+            if (pc.slot < 0)
+              store_block<PROMOTE>(&tm_y, &tm_pre, epi, o, row0, n0 + g * 32, M, N, lane, v);
+            else
+              store_part(&tm_part, o, pc.slot, prow, pcol + g * 32, lane, v);
           }
         }
       }
@@ -659,7 +662,8 @@ __global__ void __launch_bounds__(Tile<PLANES, PROMOTE>::kThreads, 1) linear_tc_
         for (int g = 0; g < kGroups; ++g) {
           if (row0 >= M || n0 + g * 32 >= N) continue;
           float* v = acc[PROMOTE ? g : 0];
-          if (pc.slot < 0) store_block(&tm_y, &tm_pre, epi, o, row0, n0 + g * 32, M, N, lane, v);
+          if (pc.slot < 0)
+            store_block<PROMOTE>(&tm_y, &tm_pre, epi, o, row0, n0 + g * 32, M, N, lane, v);
           else store_part(&tm_part, o, pc.slot, prow, pcol + g * 32, lane, v);
         }
       }
@@ -736,7 +740,7 @@ __global__ void __launch_bounds__(kJoinRows* BN / 8) linear_join_kernel(
     v[i] += bias[i];
     if (epi.pre && n + 32 * i < N) store_as(epi.pre, at + 32 * i, epi.pre_f32, v[i]);
   }
-  activate<8>(epi.act, v);
+  activate<true, 8>(epi.act, v);
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (n + 32 * i < N) store_as(epi.y, at + 32 * i, epi.y_f32, v[i] + res[i]);

@@ -331,3 +331,46 @@ def test_another_stream_two_at_once_and_captured_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(out, w))
+
+
+def _all_bf16(limit):
+    """Every bf16 value v of 2^-60 < |v| < limit: exact as an operand of any type."""
+    v = torch.arange(0, 1 << 16, device="cuda", dtype=torch.int32).to(torch.int16).view(BF16)
+    return v[(v.float().abs() < limit) & (v.float().abs() > 2.0 ** -60)]
+
+
+@pytest.mark.parametrize("name,limit", [("gelu", 13.0), ("silu", 86.0)])
+@pytest.mark.parametrize("kind", [BF16, F32])
+@pytest.mark.parametrize("as_weights", [False, True])
+def test_activations_relative_to_themselves(name, limit, kind, as_weights):
+    """fp32 results of gelu and silu on every bf16 value (pre is that value: one product with 1): within
+    2^-19 of themselves, however small. Of the polynomial 1.2e-7 (2 U); t 3 U, the polynomial's
+    steps 4 U, t and the exponential 2^-22 (4 U) and its correction 2 U, products and sums 4 U: 19
+    of 32 U. The slopes' two terms may cancel, each is as good."""
+    import product_key_memory_b200 as P
+    v = _all_bf16(limit)
+    n = v.numel()
+    one = torch.ones(1, 1, device="cuda", dtype=kind)
+    col = v.to(kind)[:, None].contiguous()
+    x, W = (one, col) if as_weights else (col, one)
+    y, pre = P.pkm_linear_forward(x, W, activation=name, out_dtype=F32, want_pre=True)
+    assert torch.equal(pre.flatten(), v.to(kind))
+    want = act(v.double(), name)
+    assert_within("y", y.flatten(), want, 2.0 ** -19 * want.abs())
+    if as_weights:
+        return
+    for r in (40, 8):                                       # rounded to bf16: whole tiles, few rows
+        xb = v[: n // r * r].view(r, -1).t().contiguous() if r == 40 else v[:r].view(r, 1)
+        Wb = torch.eye(r, device="cuda", dtype=BF16) if r == 40 else torch.ones(8, 1, device="cuda", dtype=BF16)
+        yb, _ = P.pkm_linear_forward(xb.to(BF16), Wb, activation=name)
+        wb = act((xb.double() @ Wb.double().t()), name)
+        assert_within("bf16 y", yb, wb, (half_step(BF16) + 2.0 ** -15) * wb.abs() + 2.0 ** -126)
+    g = dict(bias=torch.empty(n, device="cuda"))            # a column each: the sum of one slope
+    ones = torch.ones(1, n, device="cuda", dtype=kind)
+    P.pkm_linear_backward(one, torch.ones(n, 1, device="cuda", dtype=kind), ones, g,
+                          pre=v.to(kind)[None].contiguous(), activation=name)
+    d = v.double()
+    s = torch.sigmoid(d)
+    terms = (0.5 * torch.special.erfc(-d * 0.5 ** 0.5), d * torch.exp(-0.5 * d * d) * 0.3989422804014327) \
+        if name == "gelu" else (s, s * d * torch.sigmoid(-d))
+    assert_within("slope", g["bias"], act_slope(d, name), 2.0 ** -19 * (terms[0].abs() + terms[1].abs()))
