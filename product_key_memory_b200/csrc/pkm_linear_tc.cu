@@ -58,8 +58,7 @@ constexpr int kRows = kLinearTileM / 2;  // of a tile per CTA
 constexpr int BN = kLinearTileN;
 constexpr int kCols = BN / 2;            // columns of B per CTA
 constexpr int kK = 64;                   // K per stage: one 128-byte swizzled row of bf16
-constexpr int kSegment = 8;              // K blocks between two takings (PROMOTE)
-constexpr int kPlaneSegment = 4;         // the same where operands have planes
+constexpr int kSegment = 4;              // K blocks between two takings (PROMOTE)
 constexpr uint32_t kABytes = kRows * kK * 2;
 constexpr uint32_t kMnBlock = 64 * kK * 2;   // 64 MN x 64 K of an MN-major operand
 
@@ -429,9 +428,8 @@ __global__ void __launch_bounds__(Tile<PLANES, PROMOTE>::kThreads, 1) linear_tc_
   const int pair = blockIdx.x >> 1;
   // K blocks of a segment of a piece of k, and of the producer's walk, whose order only
   // matters with planes.
-  constexpr int kGroup = PLANES ? kPlaneSegment : kSegment;
   static_assert(!PLANES || PROMOTE, "planes: fp32 outputs");
-  const auto segment = [](int k) { return PROMOTE ? kGroup : k; };
+  const auto segment = [](int k) { return PROMOTE ? kSegment : k; };
   let_next_in();
 
   if (threadIdx.x == 0) {
@@ -473,8 +471,8 @@ __global__ void __launch_bounds__(Tile<PLANES, PROMOTE>::kThreads, 1) linear_tc_
         const TileAt mn = tile_at(pc.tile, mt, nt);
         const int m0 = mn.m * (2 * kRows) + rank * kRows;
         const int n0 = mn.n * BN + rank * kCols;
-        for (int g0 = pc.kb0; g0 < pc.kb1 && ok; g0 += kGroup) {
-          const int blocks = min(kGroup, pc.kb1 - g0);
+        for (int g0 = pc.kb0; g0 < pc.kb1 && ok; g0 += kSegment) {
+          const int blocks = min(kSegment, pc.kb1 - g0);
           for (int i = 0; i < blocks * nsteps; ++i) {
             const int step = i / blocks;
             const int k0 = (g0 + i - step * blocks) * kK;
@@ -540,7 +538,7 @@ __global__ void __launch_bounds__(Tile<PLANES, PROMOTE>::kThreads, 1) linear_tc_
       while (ok && work.next(&pc)) {
         const int kblocks = pc.kb1 - pc.kb0, seg = segment(kblocks);
         for (int k = 0; k < kblocks && ok; k += seg, ++it) {
-          const int blocks = min(seg, kblocks - k);   // with planes at most kGroup
+          const int blocks = min(seg, kblocks - k);   // with planes at most kSegment
           const int buf = it & 1;
           const uint32_t tph = (it >> 1) & 1;
           if (!mbar_wait(&tempty[buf], tph ^ 1, status, abort)) { ok = false; break; }

@@ -374,3 +374,37 @@ def test_activations_relative_to_themselves(name, limit, kind, as_weights):
     terms = (0.5 * torch.special.erfc(-d * 0.5 ** 0.5), d * torch.exp(-0.5 * d * d) * 0.3989422804014327) \
         if name == "gelu" else (s, s * d * torch.sigmoid(-d))
     assert_within("slope", g["bias"], act_slope(d, name), 2.0 ** -19 * (terms[0].abs() + terms[1].abs()))
+
+
+def _norm_error(got, ref):
+    return float((got.double() - ref).norm() / ref.norm())
+
+
+# The tensor cores cut the running sum by 2^-25 of it on average at each step of 16 terms; it is
+# taken out every 4 K blocks, 16 steps, over which it grows like the root of their number: 10.7
+# steps' worth, 10.7 * 2^-25 = 3.2e-7 of the part and so of the sum. At most 128 takings and parts
+# add their roundings' root mean square, sqrt(128) * 2^-25 * 0.6 / 3 (partial sums grow alike) =
+# 0.7e-7. What planes leave out and their own roundings are 2^-24 each in single terms, below
+# 0.1e-7 of the sum of 264 and more. A product of planes left out would be 2e-6 or more, a taking
+# half as often 6.4e-7.
+LONG_SUM = 4e-7
+
+
+@pytest.mark.parametrize("K", [264, 1001, 4096])
+@pytest.mark.parametrize("rows,cols", [(300, 520), (2400, 2100)])       # cut along K; whole tiles too
+@pytest.mark.parametrize("kind", [BF16, F32])
+def test_long_sums_in_fp32(K, rows, cols, kind):
+    """fp32 results as whole arrays: the forward over K, grad_x over N, grad_W over M."""
+    import product_key_memory_b200 as P
+    x, W, rn = _data(rows, cols, K, kind, seed=8)
+    y, _ = P.pkm_linear_forward(x, W, out_dtype=F32)
+    assert _norm_error(y, x.double() @ W.double().t()) < LONG_SUM
+    for name in ("none", "relu"):                        # relu: d takes planes, its slope is exact
+        for M, N, k in ((rows, K, cols), (K, cols, rows)):   # the long sum is N's, then M's
+            x, W, rn = _data(M, N, k, kind, seed=9)
+            gy, pre = rn(M, N).to(kind), rn(M, N).to(kind)
+            d = gy.double() * act_slope(pre.double(), name) if name != "none" else gy.double()
+            g = dict(x=torch.empty(M, k, device="cuda"), W=torch.empty(N, k, device="cuda"))
+            P.pkm_linear_backward(x, W, gy, g, pre=pre if name != "none" else None, activation=name)
+            assert _norm_error(g["x"], d @ W.double()) < LONG_SUM
+            assert _norm_error(g["W"], d.t() @ x.double()) < LONG_SUM
