@@ -378,7 +378,9 @@ size_t pkm_linear_workspace_size(const pkm_linear_shape* s, int for_backward);
  *   NULL (or the same array as y: in place)
  * Outputs (overwritten): y [M][N] out_dtype;  pre [M][N] dtype, may be NULL: what
  * pkm_linear_backward takes.
- * Products accumulate in fp32 on the tensor cores. fp32 operands are split into three bf16
+ * Products accumulate in fp32 on the tensor cores, which may cut 2^-24 of a running sum every 16
+ * terms; sums start anew every 256 terms and are added to nearest where the result is fp32, or
+ * has more than 2^15 terms. fp32 operands are split into three bf16
  * planes whose sum is the value to 2^-24, and the products above 2^-24 of the largest are
  * added; so an infinite operand makes its sums infinite or NaN, and below 2^-100 an
  * operand is its planes to 2^-134, not relatively. y is computed from pre

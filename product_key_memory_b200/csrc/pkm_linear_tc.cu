@@ -59,6 +59,10 @@ constexpr int BN = kLinearTileN;
 constexpr int kCols = BN / 2;            // columns of B per CTA
 constexpr int kK = 64;                   // K per stage: one 128-byte swizzled row of bf16
 constexpr int kSegment = 4;              // K blocks between two takings (PROMOTE)
+// Terms above which bf16 results are taken out as fp32 ones are: 2^11 cuts of 2^-24 are 2^-13, 1/32 of
+// half a step of bf16, and K = 2^20 would be all of it. 4096 x 40960 -> 4096 takes 1060 us so, 930
+// in one piece.
+constexpr int kLongSum = 1 << 15;
 constexpr uint32_t kABytes = kRows * kK * 2;
 constexpr uint32_t kMnBlock = 64 * kK * 2;   // 64 MN x 64 K of an MN-major operand
 
@@ -802,9 +806,10 @@ cudaError_t run(const LinearGemm& g, int* launches, cudaStream_t st) {
 template <bool A_MN, bool B_MN>
 cudaError_t promoted(const LinearGemm& g, int* launches, cudaStream_t st) {
   if (g.steps.products > 1) return run<A_MN, B_MN, true, true>(g, launches, st);
-  // fp32 results; a bf16 result's own rounding hides the cuts.
-  return g.epi.y_f32 || (g.epi.pre && g.epi.pre_f32) ? run<A_MN, B_MN, false, true>(g, launches, st)
-                                                     : run<A_MN, B_MN, false, false>(g, launches, st);
+  // fp32 results, and bf16 ones of very long sums; else a bf16 result's own rounding hides the cuts.
+  const bool out = g.epi.y_f32 || (g.epi.pre && g.epi.pre_f32) || g.K > kLongSum;
+  return out ? run<A_MN, B_MN, false, true>(g, launches, st)
+             : run<A_MN, B_MN, false, false>(g, launches, st);
 }
 
 }  // namespace

@@ -408,3 +408,27 @@ def test_long_sums_in_fp32(K, rows, cols, kind):
             P.pkm_linear_backward(x, W, gy, g, pre=pre if name != "none" else None, activation=name)
             assert _norm_error(g["x"], d @ W.double()) < LONG_SUM
             assert _norm_error(g["W"], d.t() @ x.double()) < LONG_SUM
+
+
+def test_bf16_results_of_very_long_sums():
+    """Sums of 65,536 positive terms on whole tiles, forward and grad_x, against the 64-bit sums
+    rounded to bf16. Cuts towards zero all have one sign. Taken out every 16 steps they are at most
+    16 * 2^-24 = 1e-6 of a sum, 0.07 of 2^16; the sums have a deviation of 107, so a step of bf16
+    (256, 2^-8 of them) is crossed by at most 0.07 * 0.4 / 107 of them: 1e-6 on the mean. Never
+    taken out, 4096 cuts of 2^-25 on average of a running sum that is half of the result are 6e-5,
+    4 of 2^16: some 2e-5 on the mean."""
+    import product_key_memory_b200 as P
+    M, wide, K = 40, 75 * 256, 1 << 16                # 75 tiles: 74 whole ones
+    g = torch.Generator(device="cuda").manual_seed(11)
+    W = torch.rand(wide, K, generator=g, device="cuda", dtype=BF16) + 0.5
+    x = torch.rand(M, K, generator=g, device="cuda").to(BF16) + 0.5
+    ref = torch.cat([x.double() @ w.double().t() for w in W.chunk(16)], 1)
+
+    def off(y):
+        return abs(float((y.double() / ref.to(BF16).double() - 1).mean()))
+    y, _ = P.pkm_linear_forward(x, W)
+    assert off(y) < 1.5e-6
+    gx = torch.empty(M, wide, device="cuda", dtype=BF16)
+    Wt = W.t().contiguous()
+    P.pkm_linear_backward(torch.empty(M, wide, device="cuda", dtype=BF16), Wt, x, dict(x=gx))
+    assert off(gx) < 1.5e-6
