@@ -807,9 +807,10 @@ template <bool A_MN, bool B_MN>
 cudaError_t promoted(const LinearGemm& g, int* launches, cudaStream_t st) {
   if (g.steps.products > 1) return run<A_MN, B_MN, true, true>(g, launches, st);
   // fp32 results, and bf16 ones of very long sums; else a bf16 result's own rounding hides the cuts.
-  const bool out = g.epi.y_f32 || (g.epi.pre && g.epi.pre_f32) || g.K > kLongSum;
-  return out ? run<A_MN, B_MN, false, true>(g, launches, st)
-             : run<A_MN, B_MN, false, false>(g, launches, st);
+  if constexpr (!A_MN)   // grad_W is fp32
+    if (!g.epi.y_f32 && !(g.epi.pre && g.epi.pre_f32) && g.K <= kLongSum)
+      return run<A_MN, B_MN, false, false>(g, launches, st);
+  return run<A_MN, B_MN, false, true>(g, launches, st);
 }
 
 }  // namespace
