@@ -24,11 +24,13 @@ __device__ __forceinline__ void clear_status(int* status) {
   if (status && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = 0;
 }
 
-// v as bf16 planes hi, mid, lo (rounded to nearest, so the sum is v to 2^-24); a value
-// that hi cannot hold as finite leaves zeros below it.
+// v as bf16 planes hi, mid, lo (rounded to nearest, so the sum is v to 2^-24; a hi that would
+// round up to infinity is cut). Infinities and NaN leave zeros below them.
 __device__ __forceinline__ void split(float v, float* p) {
+  const float inf = __uint_as_float(0x7f800000u);
   p[0] = rounded<BF16>(v);
-  const bool fine = fabsf(p[0]) < __uint_as_float(0x7f800000u);
+  if (fabsf(p[0]) == inf) p[0] = __uint_as_float(__float_as_uint(v) & 0xffff0000u);
+  const bool fine = fabsf(p[0]) < inf;
   p[1] = fine ? rounded<BF16>(v - p[0]) : 0.f;
   p[2] = fine ? rounded<BF16>(v - p[0] - p[1]) : 0.f;
 }

@@ -432,3 +432,26 @@ def test_bf16_results_of_very_long_sums():
     Wt = W.t().contiguous()
     P.pkm_linear_backward(torch.empty(M, wide, device="cuda", dtype=BF16), Wt, x, dict(x=gx))
     assert off(gx) < 1.5e-6
+
+
+@pytest.mark.parametrize("M", [40, 700])
+def test_the_largest_fp32_values(M):
+    """Finite values above the largest bf16 (3.39e38), which would round to infinity there."""
+    import product_key_memory_b200 as P
+    N, K = 72, 136
+    x, W, rn = _data(M, N, K, F32, seed=12)
+    gy = rn(M, N)
+    x[::3, 5] = 3.4e38
+    x[1::3, 7] = -3.4028e38
+    gy[3::5, 9] = 3.3999e38
+    W = W * 2.0 ** -20
+    y, _ = P.pkm_linear_forward(x, W)
+    _check_forward(x, W, None, None, "none", y, None)
+    g = dict(x=torch.empty(M, K, device="cuda"))
+    P.pkm_linear_backward(x, W, gy, g)
+    _check_backward(x, W, gy, None, "none", g)
+    g = dict(W=torch.empty(N, K, device="cuda"))
+    small = gy.clamp(-8, 8) * 2.0 ** -20
+    P.pkm_linear_backward(x, W, small, g)
+    _check_backward(x, W, small, None, "none", g)
+    assert all(bool(t.isfinite().all()) for t in (y, g["W"]))
