@@ -289,7 +289,10 @@ int pkm_slot_usage(const pkm_shape* s, const int32_t* indices, unsigned long lon
  * trained end-to-end with it): layer norm before a sub-layer, the dense sub-layers,
  * and the optimizer step. Conventions as above (caller-owned contiguous device
  * arrays, 16-byte aligned; asynchronous on `stream`; the device that owns the arrays
- * is current; arguments validated before any launch). Calls take no lock that
+ * is current; arguments validated before any launch). Arrays that are written (the workspace
+ * too) overlap no other array that the call reads or writes but where an entry says that
+ * two may be the same array (the norm and the dense layer refuse it:
+ * PKM_ERR_INVALID_ARG). Calls take no lock that
  * outlives them and share no scratch, so calls on different streams may overlap if
  * their workspaces and outputs differ.
  * ---------------------------------------------------------------------------
@@ -318,8 +321,8 @@ typedef struct {
  *   y      [rows][d]  y_dtype
  *   sum    [rows][d]  x_dtype         h; required with add, must be NULL without
  *   mean, rstd  [rows] fp32           each may be NULL
- * sum or y may be the same array as x or add where the types are equal (in place);
- * arrays overlap in no other way. Statistics are computed in fp32 from the row held
+ * sum or y may be the same array as x or add where the types are equal (in place).
+ * Statistics are computed in fp32 from the row held
  * on chip, the variance from the centred values.
  */
 int pkm_layernorm_forward(const pkm_norm_shape* s, const void* x, const void* add,
@@ -339,7 +342,7 @@ size_t pkm_norm_workspace_size(const pkm_norm_shape* s);
  *   grad_sum [rows][d] add_dtype: gradient that reaches the residual stream past the
  *            norm; may be NULL
  *   grad_x [rows][d] grad_dtype: overwritten. It is the gradient of x and of add alike.
- *            It may be the same array as grad_y or grad_sum where the types are equal.
+ *            It may be the same array as grad_y, grad_sum or x where the types are equal.
  *   grad_gamma, grad_beta [d] fp32: overwritten (zero when rows is 0); each may be NULL
  * Column sums are in fp32 in a fixed order: the result is bit-for-bit the same on every
  * run. workspace: pkm_norm_workspace_size(s) bytes, 256-byte aligned.

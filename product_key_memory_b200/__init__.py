@@ -581,7 +581,7 @@ def pkm_layernorm_backward(grad_y: torch.Tensor, x: torch.Tensor, mean: torch.Te
 
     grad_y [rows][d] fp32 or bf16; x, mean, rstd: the forward's h, mean and rstd; grad_sum
     [rows][d] fp32 or bf16: the gradient that reaches h past the norm (added to grad_x).
-    grad_x has type grad_dtype (grad_y's by default) and may be grad_y or grad_sum itself;
+    grad_x has type grad_dtype (grad_y's by default) and may be grad_y, grad_sum or x itself;
     grad_gamma and grad_beta [d] are fp32 and overwritten."""
     if x.dim() != 2:
         raise ValueError("x must be [rows][d]")

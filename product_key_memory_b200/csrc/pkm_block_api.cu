@@ -3,6 +3,8 @@
 // of its name; the stage trace covers the layer's own passes only.
 #include <math.h>
 
+#include <initializer_list>
+
 #include <nvtx3/nvToolsExt.h>
 
 #include "../../include/pkm.h"
@@ -19,6 +21,32 @@ template <int N>
 bool all_aligned16(const void* const (&ptrs)[N]) {
   for (const void* p : ptrs)
     if (!aligned16(p)) return false;
+  return true;
+}
+
+// An array of a call; empty where it is not given.
+struct Array {
+  uintptr_t at, end;
+  int dtype;
+  Array(const void* p, int64_t n, int t)
+      : at(reinterpret_cast<uintptr_t>(p)),
+        end(at + (p ? static_cast<uintptr_t>(n) * (t == PKM_BF16 ? 2 : 4) : 0)), dtype(t) {}
+};
+bool apart(const Array& a, const Array& b) {
+  return a.at == a.end || b.at == b.end || a.end <= b.at || b.end <= a.at;
+}
+// Apart, or one and the same array.
+bool apart_or_same(const Array& a, const Array& b) {
+  return (a.at == b.at && a.end == b.end && a.dtype == b.dtype) || apart(a, b);
+}
+// `outs` are apart from each other and from `ins`.
+bool all_apart(std::initializer_list<Array> outs, std::initializer_list<Array> ins) {
+  for (const Array* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Array* p = outs.begin(); p != o; ++p)
+      if (!apart(*o, *p)) return false;
+    for (const Array& i : ins)
+      if (!apart(*o, i)) return false;
+  }
   return true;
 }
 
@@ -66,6 +94,10 @@ pkm::LinearArgs linear_args(const pkm_linear_shape* s) {
   return {s->M, s->N, s->K, s->dtype, s->out_dtype, s->activation};
 }
 
+Array scratch(const pkm::LinearArgs& a, const void* workspace, bool backward) {
+  return {workspace, static_cast<int64_t>(pkm::linear_workspace_bytes(a, backward) / 4), PKM_F32};
+}
+
 }  // namespace
 
 extern "C" {
@@ -80,6 +112,14 @@ int pkm_layernorm_forward(const pkm_norm_shape* s, const void* x, const void* ad
     return PKM_ERR_INVALID_ARG;
   if (!all_aligned16({x, add, gamma, beta, y, sum, mean, rstd})) return PKM_ERR_UNSUPPORTED;
   if (s->rows == 0) return PKM_OK;
+  const int64_t n = s->rows * s->d;
+  const Array ax(x, n, s->x_dtype), aa(add, n, s->add_dtype), ay(y, n, s->y_dtype),
+      as(sum, n, s->x_dtype), am(mean, s->rows, PKM_F32), ar(rstd, s->rows, PKM_F32),
+      ag(gamma, s->d, PKM_F32), ab(beta, s->d, PKM_F32);
+  if (!all_apart({ay, as, am, ar}, {ag, ab}) || !all_apart({am, ar}, {ax, aa}) ||
+      !apart_or_same(ay, ax) || !apart_or_same(ay, aa) || !apart_or_same(as, ax) ||
+      !apart_or_same(as, aa))
+    return PKM_ERR_INVALID_ARG;
   const Range range("pkm.layernorm_forward");
   return finish(pkm::launch_layernorm_forward(norm_args(s), x, add, gamma, beta, y, sum, mean,
                                               rstd, static_cast<cudaStream_t>(stream)),
@@ -105,6 +145,15 @@ int pkm_layernorm_backward(const pkm_norm_shape* s, const void* grad_y, const vo
     return PKM_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < pkm_norm_workspace_size(s) || !aligned256(workspace))
     return PKM_ERR_WORKSPACE;
+  const int64_t n = s->rows * s->d;
+  const Array ay(grad_y, n, s->y_dtype), ax(x, n, s->x_dtype), am(mean, s->rows, PKM_F32),
+      ar(rstd, s->rows, PKM_F32), ag(gamma, s->d, PKM_F32), as(grad_sum, n, s->add_dtype),
+      ox(grad_x, n, s->grad_dtype), og(grad_gamma, s->d, PKM_F32), ob(grad_beta, s->d, PKM_F32),
+      aw(workspace, static_cast<int64_t>(pkm_norm_workspace_size(s) / sizeof(float)), PKM_F32);
+  if (s->rows > 0 &&
+      (!all_apart({ox, og, ob, aw}, {am, ar, ag}) || !all_apart({og, ob, aw}, {ay, ax, as}) ||
+       !apart_or_same(ox, ay) || !apart_or_same(ox, ax) || !apart_or_same(ox, as)))
+    return PKM_ERR_INVALID_ARG;
   const Range range("pkm.layernorm_backward");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (s->rows == 0) {
@@ -135,6 +184,11 @@ int pkm_linear_forward(const pkm_linear_shape* s, const void* x, const void* W, 
       !aligned256(workspace))
     return PKM_ERR_WORKSPACE;
   if (s->M == 0) return PKM_OK;
+  const Array ax(x, s->M * s->K, s->dtype), aw(W, static_cast<int64_t>(s->N) * s->K, s->dtype),
+      ab(bias, s->N, PKM_F32), ar(residual, s->M * s->N, s->out_dtype),
+      oy(y, s->M * s->N, s->out_dtype), op(pre, s->M * s->N, s->dtype), ow = scratch(a, workspace, false);
+  if (!all_apart({oy, op, ow}, {ax, aw, ab}) || !all_apart({op, ow}, {ar}) || !apart_or_same(oy, ar))
+    return PKM_ERR_INVALID_ARG;
   const Range range("pkm.linear_forward");
   int launches = 0;
   const cudaError_t e = pkm::launch_linear_forward(a, x, W, bias, residual, y, pre, workspace,
@@ -154,6 +208,13 @@ int pkm_linear_backward(const pkm_linear_shape* s, const void* x, const void* W,
   if (!workspace || workspace_bytes < pkm::linear_workspace_bytes(a, true) ||
       !aligned256(workspace))
     return PKM_ERR_WORKSPACE;
+  // What is read: x for grad_W, W for grad_x.
+  const Array ax(grad_W ? x : nullptr, s->M * s->K, s->dtype),
+      aw(grad_x ? W : nullptr, static_cast<int64_t>(s->N) * s->K, s->dtype),
+      ay(grad_y, s->M * s->N, s->dtype), ap(act ? pre : nullptr, s->M * s->N, s->dtype),
+      ox(grad_x, s->M * s->K, s->out_dtype), oW(grad_W, static_cast<int64_t>(s->N) * s->K, PKM_F32),
+      ob(grad_bias, s->N, PKM_F32), ow = scratch(a, workspace, true);
+  if (s->M > 0 && !all_apart({ox, oW, ob, ow}, {ax, aw, ay, ap})) return PKM_ERR_INVALID_ARG;
   const Range range("pkm.linear_backward");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (s->M == 0) {

@@ -222,3 +222,80 @@ def test_linear_binding_checks_tensors():
             call()
     with pytest.raises(P.PKMError):
         P.alloc_linear_workspace(P.make_linear_shape(4, 0, 8, torch.bfloat16))
+
+
+def _at(*places):
+    """Aligned addresses, `places` in units of 64 KiB (more than any array below)."""
+    return [ctypes.c_void_p((1 << 24) + (p << 16)) for p in places]
+
+
+@pytest.mark.parametrize("a,b,code", [
+    ("y", "gamma", -1), ("y", "beta", -1), ("y", "sum", -1), ("y", "mean", -1), ("y", "rstd", -1),
+    ("sum", "gamma", -1), ("sum", "rstd", -1), ("mean", "rstd", -1), ("mean", "x", -1),
+    ("rstd", "add", -1), ("mean", "gamma", -1), ("rstd", "beta", -1)])
+def test_norm_forward_overlaps_refused(a, b, code):
+    names = ("x", "add", "gamma", "beta", "y", "sum", "mean", "rstd")
+    arrays = dict(zip(names, _at(*range(8))))
+    arrays[a] = ctypes.c_void_p(arrays[b].value)
+    assert _forward(_norm(), **arrays) == code
+
+
+def test_norm_in_place_needs_the_same_array_and_type():
+    names = ("x", "add", "gamma", "beta", "y", "sum", "mean", "rstd")
+    for out, t in (("y", dict(y_dtype=1)), ("sum", dict(add_dtype=1))):
+        for given in ("x", "add"):
+            arrays = dict(zip(names, _at(*range(8))))
+            arrays[out] = ctypes.c_void_p(arrays[given].value + 64 * 4)      # a row further
+            assert _forward(_norm(), **arrays) == -1, (out, given)
+            arrays[out] = ctypes.c_void_p(arrays[given].value)
+            if (out, given) != ("sum", "x"):                                  # always of one type
+                assert _forward(_norm(**t), **arrays) == -1, (out, given)
+    names = ("gy", "x", "mean", "rstd", "gamma", "gsum", "gx", "gg", "gb")
+    for given in ("gy", "x", "gsum"):
+        arrays = dict(zip(names, _at(*range(9))))
+        arrays["gx"] = ctypes.c_void_p(arrays[given].value + 64 * 4)
+        assert _backward(_norm(), ws=_at(20)[0], **arrays) == -1, given
+        arrays["gx"] = ctypes.c_void_p(arrays[given].value)
+        assert _backward(_norm(grad_dtype=1), ws=_at(20)[0], **arrays) == -1, given
+
+
+@pytest.mark.parametrize("a,b", [
+    ("gx", "mean"), ("gx", "rstd"), ("gx", "gamma"), ("gx", "gg"), ("gx", "gb"), ("gg", "gb"),
+    ("gg", "gy"), ("gb", "x"), ("gg", "gsum"), ("gg", "gamma"), ("gb", "mean")])
+def test_norm_backward_overlaps_refused(a, b):
+    names = ("gy", "x", "mean", "rstd", "gamma", "gsum", "gx", "gg", "gb")
+    arrays = dict(zip(names, _at(*range(9))))
+    arrays[a] = ctypes.c_void_p(arrays[b].value)
+    assert _backward(_norm(), ws=_at(20)[0], **arrays) == -1
+    for name in names:
+        arrays = dict(zip(names, _at(*range(9))))
+        assert _backward(_norm(), ws=arrays[name], **arrays) == -1, name
+
+
+@pytest.mark.parametrize("M", [3, 100])
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_linear_overlaps_refused(M, dtype):
+    s = _linear(M=M, N=80, K=80, dtype=dtype, out_dtype=dtype, activation=2)
+    names = ("x", "W", "bias", "residual", "y", "pre")
+    for a, b in (("y", "x"), ("y", "W"), ("y", "bias"), ("y", "pre"), ("pre", "x"), ("pre", "W"),
+                 ("pre", "bias"), ("pre", "residual")):
+        arrays = dict(zip(names, _at(*range(6))))
+        arrays[a] = ctypes.c_void_p(arrays[b].value)
+        assert _linear_forward(s, ws=_at(20)[0], **arrays) == -1, (a, b)
+    arrays = dict(zip(names, _at(*range(6))))
+    arrays["y"] = ctypes.c_void_p(arrays["residual"].value + 16)          # partly
+    assert _linear_forward(s, ws=_at(20)[0], **arrays) == -1
+    for name in names:
+        arrays = dict(zip(names, _at(*range(6))))
+        assert _linear_forward(s, ws=arrays[name], **arrays) == -1, name
+    names = ("x", "W", "gy", "pre", "gx", "gW", "gb")
+    for a in ("gx", "gW", "gb"):
+        for b in names:
+            if a == b:
+                continue
+            arrays = dict(zip(names, _at(*range(7))))
+            arrays[a] = ctypes.c_void_p(arrays[b].value)
+            assert _linear_backward(s, ws=_at(200)[0], **arrays) == -1, (a, b)
+    for name in names:
+        arrays = dict(zip(names, _at(*range(7))))
+        assert _linear_backward(s, ws=arrays[name], **arrays) == -1, name

@@ -310,3 +310,21 @@ def test_backward_rows_far_from_zero(d, rows, xt, offset):
     xhat = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
     # A term has two roundings of xhat and one of its product (or none, fused), the sum `rows` at most.
     assert_within("grad_gamma", got[1], rg, (rows + 3) * U * (gy.double() * xhat).abs().sum(0))
+
+
+@pytest.mark.parametrize("d", [64, 333, 1000, 5001])
+def test_backward_over_x(d):
+    import product_key_memory_b200 as P
+    x, gsum, gamma, beta, rn = _data(300, d, BF16, F32, seed=d)
+    gy = rn(300, d)
+    _, _, mean, rstd = P.pkm_layernorm_forward(x, gamma, beta)
+    want = P.pkm_layernorm_backward(gy, x, mean, rstd, gamma, grad_sum=gsum, grad_dtype=BF16)
+    a = x.clone()
+    got = P.pkm_layernorm_backward(gy, a, mean, rstd, gamma, grad_sum=gsum, grad_x=a)
+    assert got[0].data_ptr() == a.data_ptr() and all(torch.equal(p, q) for p, q in zip(got, want))
+    with pytest.raises(P.PKMError):                        # two results in one array
+        P.pkm_layernorm_forward(x, gamma, beta, add=gsum, out=a, sum_out=a)
+    W = torch.ones(d, d, device="cuda", dtype=BF16)
+    for kw in (dict(out=x), dict(pre=x), dict(out=a, pre=a)):
+        with pytest.raises(P.PKMError):
+            P.pkm_linear_forward(x, W, **kw)
