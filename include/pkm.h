@@ -330,7 +330,7 @@ int pkm_layernorm_forward(const pkm_norm_shape* s, const void* x, const void* ad
                           float* rstd, void* stream);
 
 /* Bytes of workspace pkm_layernorm_backward needs; 0 if the shape is invalid. Only rows
- * and d are read. */
+ * and d are read. A workspace for some rows serves fewer as well. */
 size_t pkm_norm_workspace_size(const pkm_norm_shape* s);
 
 /*

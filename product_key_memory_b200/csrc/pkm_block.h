@@ -60,8 +60,9 @@ cudaError_t launch_layernorm_forward(const NormArgs& a, const void* x, const voi
                                      const float* gamma, const float* beta, void* y, void* sum,
                                      float* mean, float* rstd, cudaStream_t st);
 
-// Partial column sums of the backward: blocks (at most) x [2][d] fp32.
-int norm_backward_blocks(int64_t rows, int d);
+// Partial column sums of the backward: [2][d] fp32 for each of at most so many blocks. Never more
+// for fewer rows (the blocks themselves may be, in narrow rows: their groups are whole warps).
+int norm_workspace_blocks(int64_t rows);
 cudaError_t launch_layernorm_backward(const NormArgs& a, const void* grad_y, const void* x,
                                       const float* mean, const float* rstd, const float* gamma,
                                       const void* grad_sum, void* grad_x, float* grad_gamma,

@@ -128,7 +128,7 @@ int pkm_layernorm_forward(const pkm_norm_shape* s, const void* x, const void* ad
 
 size_t pkm_norm_workspace_size(const pkm_norm_shape* s) {
   if (validate_norm_size(s) != PKM_OK) return 0;
-  return static_cast<size_t>(pkm::norm_backward_blocks(s->rows, s->d)) * 2 * s->d * sizeof(float);
+  return static_cast<size_t>(pkm::norm_workspace_blocks(s->rows)) * 2 * s->d * sizeof(float);
 }
 
 int pkm_layernorm_backward(const pkm_norm_shape* s, const void* grad_y, const void* x,

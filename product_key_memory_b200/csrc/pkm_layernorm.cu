@@ -718,8 +718,7 @@ __global__ void __launch_bounds__(32 * kStrands) layernorm_columns_kernel(const 
 
 // How the backward's rows are shared out: groups of T threads with C accesses of 8 (or, odd
 // widths, 1) elements each and R rows at a time, `per` groups a block of at most 512
-// threads, and at most one block for each of the 148 SMs of a B200 (the workspace's size
-// depends on the number of blocks, so on the sizes alone).
+// threads, and at most one block for each of the 148 SMs of a B200.
 struct NormGroups {
   int T, C, R, per, blocks;
 };
@@ -821,14 +820,16 @@ cudaError_t launch_layernorm_forward(const NormArgs& a, const void* x, const voi
   return yf ? pick_fwd<BF16, F32>(l) : pick_fwd<BF16, BF16>(l);
 }
 
-int norm_backward_blocks(int64_t rows, int d) { return norm_groups(rows, d).blocks; }
+int norm_workspace_blocks(int64_t rows) {
+  return static_cast<int>(rows < 1 ? 1 : (rows < 148 ? rows : 148));
+}
 
 cudaError_t launch_layernorm_backward(const NormArgs& a, const void* grad_y, const void* x,
                                       const float* mean, const float* rstd, const float* gamma,
                                       const void* grad_sum, void* grad_x, float* grad_gamma,
                                       float* grad_beta, float* part, cudaStream_t st) {
   const bool sums = grad_gamma || grad_beta;
-  BwdLaunch l{a.rows, a.d, a.add_dtype == 0, norm_backward_blocks(a.rows, a.d), grad_y, x,
+  BwdLaunch l{a.rows, a.d, a.add_dtype == 0, norm_groups(a.rows, a.d).blocks, grad_y, x,
               grad_sum, mean, rstd, gamma, grad_x, sums ? part : nullptr, st};
   const bool xf = a.x_dtype == 0, gf = a.y_dtype == 0, of = a.grad_dtype == 0;
   cudaError_t e;

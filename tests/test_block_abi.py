@@ -299,3 +299,10 @@ def test_linear_overlaps_refused(M, dtype):
     for name in names:
         arrays = dict(zip(names, _at(*range(7))))
         assert _linear_backward(s, ws=arrays[name], **arrays) == -1, name
+
+
+@pytest.mark.parametrize("d", [8, 40, 64, 65, 1024, 2001])
+def test_norm_workspace_serves_fewer_rows(d):
+    sizes = [int(P.lib().pkm_norm_workspace_size(ctypes.byref(_norm(rows=r, d=d))))
+             for r in list(range(3000)) + [20000, 1 << 30]]
+    assert sizes == sorted(sizes)
