@@ -383,12 +383,12 @@ size_t pkm_linear_workspace_size(const pkm_linear_shape* s, int for_backward);
  * pkm_linear_backward takes.
  * Products accumulate in fp32 on the tensor cores, which may cut 2^-24 of a running sum every 16
  * terms; sums start anew every 256 terms and are added to nearest where the result is fp32, or
- * has more than 2^15 terms. fp32 operands are split into three bf16
- * planes whose sum is the value to 2^-24, and the products above 2^-24 of the largest are
- * added; so an infinite operand makes its sums infinite or NaN, and below 2^-100 an
- * operand is its planes to 2^-134, not relatively. y is computed from pre
- * before pre is rounded. Few rows (up to 8, in bf16 16 or 32) take kernels that stream W
- * once. M N and M K are below 2^38.
+ * has more than 2^15 terms. fp32 operands are split into three bf16 planes whose sum is the
+ * value to 2^-24, and the products above 2^-24 of the largest are added; so an infinite
+ * operand makes its sums infinite or NaN, and below 2^-100 an operand is its planes to
+ * 2^-134, not relatively. Small fp32 layers multiply in fp32 on the CUDA cores instead, with
+ * a sum of its own for every 32 terms. y is computed from pre before pre is rounded. Few rows
+ * (up to 8, in bf16 16 or 32) take kernels that stream W once. M N and M K are below 2^38.
  * workspace: pkm_linear_workspace_size(s, 0) bytes, 256-byte aligned; its status word
  * (pkm_device_status) records a bounded wait that ran out.
  */

@@ -621,7 +621,7 @@ Layout layout(const LinearArgs& a, bool backward) {
 bool linear_small(const LinearArgs& a) { return a.M <= kSmallM || linear_rows(a); }
 
 size_t linear_workspace_bytes(const LinearArgs& a, bool backward) {
-  if (a.M == 0 || (!backward && linear_small(a))) return kStatusBytes;
+  if (a.M == 0 || (!backward && linear_small(a)) || linear_f32(a, backward)) return kStatusBytes;
   return layout(a, backward).total;
 }
 
@@ -648,6 +648,9 @@ cudaError_t launch_linear_forward(const LinearArgs& a, const void* x, const void
     return vec ? run_small<BF16, 8>(M, x, W, a.N, a.K, epi, first, st)
                : run_small<BF16, 1>(M, x, W, a.N, a.K, epi, first, st);
   }
+  if (linear_f32(a, false))
+    return launch_f32_forward(a, static_cast<const float*>(x), static_cast<const float*>(W), epi,
+                              status, launches, st);
   const Layout l = layout(a, false);
   char* ws = static_cast<char*>(workspace);
   const int64_t ld = pad8(a.K);
@@ -671,6 +674,10 @@ cudaError_t launch_linear_backward(const LinearArgs& a, const void* x, const voi
                                    const void* grad_y, const void* pre, void* grad_x,
                                    float* grad_W, float* grad_bias, void* workspace,
                                    int* launches, cudaStream_t st) {
+  if (linear_f32(a, true))
+    return launch_f32_backward(a, static_cast<const float*>(x), static_cast<const float*>(W),
+                               static_cast<const float*>(grad_y), static_cast<const float*>(pre),
+                               grad_x, grad_W, grad_bias, static_cast<int*>(workspace), launches, st);
   const Layout l = layout(a, true);
   char* ws = static_cast<char*>(workspace);
   int* status = static_cast<int*>(workspace);

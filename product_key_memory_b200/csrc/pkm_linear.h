@@ -1,5 +1,6 @@
 // pkm_linear.h -- internal interface of the dense layer: the tensor-core product
-// (pkm_linear_tc.cu), the passes around it and the small-batch kernel (pkm_linear.cu).
+// (pkm_linear_tc.cu), the passes around it and the small-batch kernel (pkm_linear.cu), the products
+// of small fp32 layers (pkm_linear_f32.cu).
 #pragma once
 
 #include "pkm_block.h"
@@ -66,6 +67,15 @@ struct LinearArgs {
 constexpr int kLinearMaxWidth = 1 << 20;   // N and K
 
 bool linear_small(const LinearArgs& a);    // the forward's small-batch kernel takes it
+
+// Small fp32 layers on the CUDA cores (pkm_linear_f32.cu).
+bool linear_f32(const LinearArgs& a, bool backward);
+cudaError_t launch_f32_forward(const LinearArgs& a, const float* x, const float* W,
+                               const LinearEpilogue& epi, int* status, int* launches,
+                               cudaStream_t st);
+cudaError_t launch_f32_backward(const LinearArgs& a, const float* x, const float* W,
+                                const float* grad_y, const float* pre, void* grad_x, float* grad_W,
+                                float* grad_bias, int* status, int* launches, cudaStream_t st);
 size_t linear_workspace_bytes(const LinearArgs& a, bool backward);
 cudaError_t launch_linear_forward(const LinearArgs& a, const void* x, const void* W,
                                   const float* bias, const void* residual, void* y, void* pre,

@@ -455,3 +455,76 @@ def test_the_largest_fp32_values(M):
     P.pkm_linear_backward(x, W, small, g)
     _check_backward(x, W, small, None, "none", g)
     assert all(bool(t.isfinite().all()) for t in (y, g["W"]))
+
+
+# Small fp32 layers: each height of a tile (16, 32, 64 rows), one to eight shares of K, shares that end
+# inside a step, widths next to a tile's 64, and both sides of the limit to the tensor cores.
+SMALL_F32 = [(9, 1, 1), (9, 63, 4351), (16, 64, 33), (17, 65, 31), (32, 129, 300), (33, 40, 1000),
+             (64, 64, 64), (65, 200, 8), (100, 33, 2000), (500, 100, 129), (777, 93, 320),
+             (1200, 70, 40), (300, 400, 264), (512, 512, 512), (600, 600, 600), (58, 3136, 40)]
+
+
+@pytest.mark.parametrize("M,N,K", SMALL_F32)
+@pytest.mark.parametrize("name", ACTS)
+def test_small_fp32_layers(M, N, K, name):
+    import product_key_memory_b200 as P
+    x, W, rn = _data(M, N, K, F32, seed=13)
+    yt, xt = ((F32, BF16), (BF16, F32), (F32, F32))[(M + N) % 3]
+    bias, residual = rn(N), rn(M, N).to(yt)
+    out, check_out = guarded((M, N), yt)
+    pre, check_pre = guarded((M, N), F32)
+    ws = P.alloc_linear_workspace(P.make_linear_shape(M, N, K, F32, yt, name)).fill_(255)
+    P.pkm_linear_forward(x, W, bias, residual, name, out=out, pre=pre, workspace=ws)
+    assert P.pkm_device_status(ws) == 0
+    _check_forward(x, W, bias, residual, name, out, pre)
+    again, _ = P.pkm_linear_forward(x, W, bias, residual.clone(), name, out_dtype=yt)
+    assert torch.equal(again, out)
+    check_out()
+    check_pre()
+    gy, pre = rn(M, N), rn(M, N) if name != "none" else None
+    gx, check_x = guarded((M, K), xt)
+    gW, check_W = guarded((N, K), F32)
+    gb, check_b = guarded((N,), F32)
+    ws = P.alloc_linear_workspace(P.make_linear_shape(M, N, K, F32, xt, name), True).fill_(255)
+    grads = dict(x=gx, W=gW, bias=gb)
+    P.pkm_linear_backward(x, W, gy, grads, pre=pre, activation=name, workspace=ws)
+    assert P.pkm_device_status(ws) == 0
+    _check_backward(x, W, gy, pre, name, grads)
+    for check in (check_x, check_W, check_b):
+        check()
+    for keys in (("x",), ("W",), ("bias",), ("x", "bias")):
+        some = {k: torch.full_like(grads[k], 9.0) for k in keys}
+        P.pkm_linear_backward(x, W, gy, some, pre=pre, activation=name)
+        assert all(torch.equal(some[k], grads[k]) for k in keys), keys
+
+
+def test_small_fp32_layers_on_streams_and_in_a_graph():
+    import product_key_memory_b200 as P
+    x, W, rn = _data(200, 136, 500, F32, seed=14)
+    gy = rn(200, 136)
+
+    def both(stream=None):
+        y, pre = P.pkm_linear_forward(x, W, activation="silu", want_pre=True, stream=stream)
+        g = dict(x=torch.empty_like(x), W=torch.empty_like(W), bias=torch.empty(136, device="cuda"))
+        P.pkm_linear_backward(x, W, gy, g, pre=pre, activation="silu", stream=stream)
+        return [y, pre, *g.values()]
+    want = both()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = [both(s) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
+    with torch.cuda.stream(streams[0]):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=streams[0]):
+            out = both()
+    for t in out:
+        t.fill_(3.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+    bad = x.clone()
+    bad[7, 3] = float("nan")
+    y, _ = P.pkm_linear_forward(bad, W, activation="silu")
+    keep = torch.arange(200, device="cuda") != 7
+    assert torch.equal(y[keep], want[0][keep]) and bool(y[7].isnan().all())
