@@ -390,7 +390,8 @@ size_t pkm_linear_workspace_size(const pkm_linear_shape* s, int for_backward);
  * a sum of its own for every 32 terms. y is computed from pre before pre is rounded. Few rows
  * (up to 8, in bf16 16 or 32) take kernels that stream W once. M N and M K are below 2^38.
  * workspace: pkm_linear_workspace_size(s, 0) bytes, 256-byte aligned; its status word
- * (pkm_device_status) records a bounded wait that ran out.
+ * (pkm_device_status) records a bounded wait that ran out. A call without work (M = 0, or in the
+ * backward no gradient asked for) launches no kernel and leaves the status word as it was.
  */
 int pkm_linear_forward(const pkm_linear_shape* s, const void* x, const void* W, const float* bias,
                        const void* residual, void* y, void* pre, void* workspace,
