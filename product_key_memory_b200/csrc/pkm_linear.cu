@@ -392,8 +392,8 @@ cudaError_t make_planes(const PlanesOf& a, const PlanesOf& b, int dtype, int col
 // Block: 256 columns (32 lanes of 8) x `per` rows (8 warps, every eighth row each). d is
 // written as NP planes (NP = 0: not needed) and its column sums as one partial row per block
 // row (part NULL: not needed). Bound by HBM and the slope's arithmetic together: 4096 x 6400
-// bf16, gelu, three planes, 262 MB: 55 us with four blocks an SM, 60 with two of which each
-// thread has two rows in flight.
+// bf16, gelu, three planes, 262 MB: 58 us with four blocks an SM (two, of which
+// each thread has two rows in flight, took 5 us more).
 // Rows of a block: 64, or fewer (a warp then has fewer one after the other) until there are two
 // blocks for each of the 148 SMs (the whole backward of 777 x 4096 -> 1024 bf16 gelu: 58 us on the
 // device, with 64 rows 69).
