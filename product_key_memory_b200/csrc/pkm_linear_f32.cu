@@ -65,7 +65,7 @@ template <bool K_INNER, int R> struct Places {
 __device__ __forceinline__ float load_or_zero(const float* p, bool in) {
   float v;
   asm volatile("{\n\t.reg .pred in;\n\tsetp.ne.b32 in, %2, 0;\n\tmov.f32 %0, 0f00000000;\n\t"
-               "@in ld.global.nc.f32 %0, [%1];\n\t}"
+               "@in ld.global.f32 %0, [%1];\n\t}"
                : "=f"(v) : "l"(p), "r"(static_cast<int>(in)) : "memory");
   return v;
 }
