@@ -403,9 +403,9 @@ int pkm_linear_forward(const pkm_linear_shape* s, const void* x, const void* W, 
  * each overwritten and each may be NULL (not computed). The residual's gradient is grad_y.
  *   x, W as in the forward; grad_y [M][N] dtype; pre [M][N] dtype as the forward wrote it
  *   (not read, may be NULL, without an activation)
- * d is an fp32 value. With an activation and in fp32 layers it enters the products as three
- * bf16 planes whose sum is d to 2^-24; in a bf16 layer's bf16 grad_x as two, d to 2^-16
- * (relu: d is bf16 itself). Column sums add in a fixed order; all results are
+ * d is an fp32 value. With an activation and in fp32 layers (but small ones) it enters the
+ * products as three bf16 planes whose sum is d to 2^-24; in a bf16 layer's bf16 grad_x as two,
+ * d to 2^-16 (relu: d is bf16 itself). Column sums add in a fixed order; all results are
  * bit-for-bit the same on every run.
  * workspace: pkm_linear_workspace_size(s, 1) bytes, 256-byte aligned, status word as above.
  */

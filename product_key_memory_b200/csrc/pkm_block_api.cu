@@ -94,8 +94,8 @@ pkm::LinearArgs linear_args(const pkm_linear_shape* s) {
   return {s->M, s->N, s->K, s->dtype, s->out_dtype, s->activation};
 }
 
-Array scratch(const pkm::LinearArgs& a, const void* workspace, bool backward) {
-  return {workspace, static_cast<int64_t>(pkm::linear_workspace_bytes(a, backward) / 4), PKM_F32};
+Array scratch(const void* workspace, size_t bytes) {
+  return {workspace, static_cast<int64_t>(bytes / sizeof(float)), PKM_F32};
 }
 
 }  // namespace
@@ -143,13 +143,13 @@ int pkm_layernorm_backward(const pkm_norm_shape* s, const void* grad_y, const vo
     return PKM_ERR_INVALID_ARG;
   if (!all_aligned16({grad_y, x, mean, rstd, gamma, grad_sum, grad_x, grad_gamma, grad_beta}))
     return PKM_ERR_UNSUPPORTED;
-  if (!workspace || workspace_bytes < pkm_norm_workspace_size(s) || !aligned256(workspace))
-    return PKM_ERR_WORKSPACE;
+  const size_t need = pkm_norm_workspace_size(s);
+  if (!workspace || workspace_bytes < need || !aligned256(workspace)) return PKM_ERR_WORKSPACE;
   const int64_t n = s->rows * s->d;
   const Array ay(grad_y, n, s->y_dtype), ax(x, n, s->x_dtype), am(mean, s->rows, PKM_F32),
       ar(rstd, s->rows, PKM_F32), ag(gamma, s->d, PKM_F32), as(grad_sum, n, s->add_dtype),
       ox(grad_x, n, s->grad_dtype), og(grad_gamma, s->d, PKM_F32), ob(grad_beta, s->d, PKM_F32),
-      aw(workspace, static_cast<int64_t>(pkm_norm_workspace_size(s) / sizeof(float)), PKM_F32);
+      aw = scratch(workspace, need);
   if (s->rows > 0 &&
       (!all_apart({ox, og, ob, aw}, {am, ar, ag}) || !all_apart({og, ob, aw}, {ay, ax, as}) ||
        !apart_or_same(ox, ay) || !apart_or_same(ox, ax) || !apart_or_same(ox, as)))
@@ -180,13 +180,12 @@ int pkm_linear_forward(const pkm_linear_shape* s, const void* x, const void* W, 
   if (!W || (s->M > 0 && (!x || !y))) return PKM_ERR_INVALID_ARG;
   if (!all_aligned16({x, W, bias, residual, y, pre})) return PKM_ERR_UNSUPPORTED;
   const pkm::LinearArgs a = linear_args(s);
-  if (!workspace || workspace_bytes < pkm::linear_workspace_bytes(a, false) ||
-      !aligned256(workspace))
-    return PKM_ERR_WORKSPACE;
+  const size_t need = pkm::linear_workspace_bytes(a, false);
+  if (!workspace || workspace_bytes < need || !aligned256(workspace)) return PKM_ERR_WORKSPACE;
   if (s->M == 0) return PKM_OK;
   const Array ax(x, s->M * s->K, s->dtype), aw(W, static_cast<int64_t>(s->N) * s->K, s->dtype),
       ab(bias, s->N, PKM_F32), ar(residual, s->M * s->N, s->out_dtype),
-      oy(y, s->M * s->N, s->out_dtype), op(pre, s->M * s->N, s->dtype), ow = scratch(a, workspace, false);
+      oy(y, s->M * s->N, s->out_dtype), op(pre, s->M * s->N, s->dtype), ow = scratch(workspace, need);
   if (!all_apart({oy, op, ow}, {ax, aw, ab}) || !all_apart({op, ow}, {ar}) || !apart_or_same(oy, ar))
     return PKM_ERR_INVALID_ARG;
   const Range range("pkm.linear_forward");
@@ -205,15 +204,14 @@ int pkm_linear_backward(const pkm_linear_shape* s, const void* x, const void* W,
   if (!W || (s->M > 0 && (!x || !grad_y || (act && !pre)))) return PKM_ERR_INVALID_ARG;
   if (!all_aligned16({x, W, grad_y, pre, grad_x, grad_W, grad_bias})) return PKM_ERR_UNSUPPORTED;
   const pkm::LinearArgs a = linear_args(s);
-  if (!workspace || workspace_bytes < pkm::linear_workspace_bytes(a, true) ||
-      !aligned256(workspace))
-    return PKM_ERR_WORKSPACE;
+  const size_t need = pkm::linear_workspace_bytes(a, true);
+  if (!workspace || workspace_bytes < need || !aligned256(workspace)) return PKM_ERR_WORKSPACE;
   // What is read: x for grad_W, W for grad_x.
   const Array ax(grad_W ? x : nullptr, s->M * s->K, s->dtype),
       aw(grad_x ? W : nullptr, static_cast<int64_t>(s->N) * s->K, s->dtype),
       ay(grad_y, s->M * s->N, s->dtype), ap(act ? pre : nullptr, s->M * s->N, s->dtype),
       ox(grad_x, s->M * s->K, s->out_dtype), oW(grad_W, static_cast<int64_t>(s->N) * s->K, PKM_F32),
-      ob(grad_bias, s->N, PKM_F32), ow = scratch(a, workspace, true);
+      ob(grad_bias, s->N, PKM_F32), ow = scratch(workspace, need);
   if (s->M > 0 && !all_apart({ox, oW, ob, ow}, {ax, aw, ay, ap})) return PKM_ERR_INVALID_ARG;
   const Range range("pkm.linear_backward");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
